@@ -49,7 +49,8 @@ typedef enum tq_status {
 
 typedef enum tq_dtype {
     TQ_F16 = 0,               /* IEEE binary16 */
-    TQ_F32 = 1                /* IEEE binary32 */
+    TQ_F32 = 1,               /* IEEE binary32 */
+    TQ_BF16 = 2               /* bfloat16 (the paged-cache entry points) */
 } tq_dtype;
 
 /* Message for the last non-TQ_OK status returned on this thread ("" if none). */
@@ -413,6 +414,160 @@ tq_status tq_attend_qjl_workspace_bytes(const tq_attend_args* args, size_t* byte
  */
 tq_status tq_attend_decode_qjl(const tq_codec* codec, const tq_attend_args* args, const tq_qjl_keys* keys,
                                void* stream);
+
+/* --------------------------------------------------------------------------------------------------
+ * The paged cache: block tables and slots, uncompressed pages, page selection.
+ *
+ * A page is one block of 16 tokens of the paged layout above.  Head page e = page * num_kv_heads + h is the 16 rows
+ * of kv head h in a page; a slot e * 16 + t % 16 is the pool row of one token and kv head, for compressed pools
+ * (tq_encode_k, tq_encode_v) and uncompressed ones alike.  An uncompressed pool is
+ * [num_pages][num_kv_heads][16][head_dim] of binary16 or bfloat16.
+ *
+ * One decode step over a paged cache: tq_plan_pages gives every request's new tokens their pages and slots;
+ * tq_encode_k / tq_encode_v, or tq_append_pages for layers kept uncompressed, store them; tq_attend_decode or
+ * tq_attend_pages read the cache.  To read only part of a long cache, tq_append_pages keeps channel bounds of every
+ * page's keys, tq_select_pages picks pages by them, and either attention reads the picked ones.
+ *
+ * No call synchronises, allocates, or keeps anything between calls, so each can be captured into a CUDA graph and
+ * replayed with new contents of the same buffers.  Page ids that name no page of a pool are never followed: their
+ * tokens are left out.
+ * ------------------------------------------------------------------------------------------------ */
+
+typedef struct tq_plan_args {
+    int batch;                 /* requests, 1 .. 2^24 */
+    int num_kv_heads;          /* 1 .. 1024 */
+    int max_blocks;            /* columns of block_table */
+    int num_pages;             /* pages of the pool; entries of free_pages */
+    int64_t max_tokens;        /* input rows (tokens) the caller has: slots for this many are written */
+    const int32_t* new_lens;   /* device [batch]: tokens to add; 0 none; negative: the request is finished */
+    const int32_t* seq_lens;   /* device [batch]: tokens cached so far (clamped to 0 .. max_blocks * 16) */
+    int32_t* block_table;      /* device [batch][max_blocks], updated in place: entries of new pages are written */
+    int32_t* free_pages;       /* device [num_pages], updated in place: a ring of free page ids */
+    const int32_t* free_state; /* device [2]: index of the ring's first free page, number of free pages */
+    int64_t* slots;            /* out, device [max_tokens][num_kv_heads] (may be NULL if max_tokens is 0) */
+    int32_t* row_start;        /* out, device [batch + 1]: first input row of each request; the last entry is their sum */
+    int32_t* start_pos;        /* out, device [batch]: position of a request's first new token, -1 if it adds none
+                                  because it was refused or is finished */
+    int32_t* seq_lens_out;     /* out, device [batch]: tokens after this step (may be seq_lens) */
+    int32_t* free_state_out;   /* out, device [2] (may be free_state) */
+} tq_plan_args;
+
+/*
+ * tq_plan_pages -- block tables and slots of one step, from the requests' lengths, on the GPU.  The input rows of
+ * request b are row_start[b] .. row_start[b + 1] - 1 (row_start: running sum of max(new_lens, 0)); its i-th new token
+ * is token seq_lens[b] + i and gets
+ *   slots[(row_start[b] + i) * num_kv_heads + h] = (block_table[b][t / 16] * num_kv_heads + h) * 16 + t % 16.
+ *   - Pages: a request needs ceil((len + new) / 16) - ceil(len / 16) pages.  In the order of the batch, it is refused
+ *     if its tokens do not fit its table row or max_tokens, or if it needs pages and the needs up to and including
+ *     it exceed the free count (so no later request that needs pages gets any either).  A refused request adds
+ *     nothing; its length and table row stay as they are.
+ *   - New pages come from the ring's start in the order of the batch.  A finished request's pages (the
+ *     ceil(len / 16) entries of its table row) are put at the ring's end, for later calls, and its length becomes 0.
+ *   - Rows of refused requests, rows from row_start[batch] on, and rows whose table entry names no page get slot -1,
+ *     which tq_encode_k, tq_encode_v and tq_append_pages skip.
+ * Preconditions not checked: a page id is owned once (in one table row or in the ring), and seq_lens are those of
+ * the table rows.  row_start saturates at 2^31 - 1 (requests from there on are refused).
+ * Errors: TQ_ERR_INVALID_ARG for counts out of range, NULL or misaligned pointers.
+ */
+tq_status tq_plan_pages(const tq_plan_args* args, void* stream);
+
+typedef struct tq_append_args {
+    int dtype;                 /* TQ_F16 or TQ_BF16: k, v, pools and bounds */
+    int head_dim;              /* 64, 128 or 256 */
+    int num_kv_heads;
+    int num_pages;             /* pages of the pools and of bounds */
+    int64_t num_tokens;        /* input rows (0 is a no-op) */
+    const void* k;             /* device: token t, kv head h at k + t * k_token_stride + h * k_head_stride (elements) */
+    const void* v;             /* device, the same with its own strides; needed if v_pool is given */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;   /* multiples of 8 */
+    const int64_t* slots;      /* device [num_tokens][num_kv_heads], e.g. from tq_plan_pages; slots below 0 or past the
+                                  pool's rows skip the row */
+    void* k_pool;              /* nullable: device [num_pages][num_kv_heads][16][head_dim] */
+    void* v_pool;              /* nullable, the same shape */
+    void* bounds;              /* nullable: device [num_pages][num_kv_heads][2][head_dim]: lowest, highest key */
+} tq_append_args;
+
+/*
+ * tq_append_pages -- store new keys and values of a step in uncompressed pools, and keep the channel bounds of the
+ * pages' keys: bounds[page][h][0][c] and [1][c] are the minimum and maximum over the page's keys of channel c.  A
+ * page whose first token (slot % 16 == 0) is among the rows starts anew; others extend the bounds they have.  For a
+ * compressed cache only bounds is given and the rows go through tq_encode_k.
+ * Rows not named by a slot are left as they were.  Tokens of one page and kv head must be consecutive input rows, as
+ * tq_plan_pages lays them out (a page that appears in two places in one call gets undefined bounds); if a slot appears
+ * twice, one of its rows is stored.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype).
+ */
+tq_status tq_append_pages(const tq_append_args* args, void* stream);
+
+typedef struct tq_select_args {
+    int dtype;                 /* TQ_F16 or TQ_BF16: q and bounds */
+    int batch, num_q_heads, num_kv_heads, head_dim;
+    int max_blocks;            /* columns of block_table */
+    int num_pages;             /* pages of bounds */
+    int budget;                /* pages kept per (sequence, kv head) */
+    int keep_first, keep_last; /* pages at the start and at the end that are kept whatever their score
+                                  (keep_first >= 0, keep_last >= 1, keep_first + keep_last <= budget) */
+    const void* q;             /* device [batch] rows of [num_q_heads][head_dim], q_stride elements apart */
+    int64_t q_stride;          /* a multiple of 8 */
+    const void* bounds;        /* device [num_pages][num_kv_heads][2][head_dim] (tq_append_pages) */
+    const int32_t* block_table;/* device [batch][max_blocks] */
+    const int32_t* seq_lens;   /* device [batch] (clamped to 0 .. max_blocks * 16) */
+    int32_t* pages;            /* out, device [batch][num_kv_heads][budget]: head pages in ascending order, then -1 */
+    int32_t* lens;             /* out, device [batch][num_kv_heads]: tokens of the listed pages */
+} tq_select_args;
+
+/*
+ * tq_select_pages -- the pages a decode step attends to.  For each page of a sequence and each kv head,
+ *   score = max over the group's query heads of  sum_c max(q_c * bounds[0][c], q_c * bounds[1][c]),
+ * an upper bound of q . k over the page's keys.  The first keep_first and last keep_last pages are kept; the rest of
+ * `budget` goes to the highest scores, ties to the lower index.  A sequence of at most `budget` pages keeps all.
+ * lens counts the tokens of the listed pages (every page is full but a sequence's last, which is always listed last),
+ * so pages and lens are a block table and lengths with one row per (sequence, kv head).  Read them with
+ * tq_attend_pages (selected = 1), or with tq_attend_decode on the compressed pools as batch * num_kv_heads sequences
+ * of one kv head: a head page is a page of a pool with one kv head.
+ * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
+ * result is the same on every run and for every shape of the call.  A score that is not a number ranks last.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8, max_blocks too large).
+ */
+tq_status tq_select_pages(const tq_select_args* args, void* stream);
+
+typedef struct tq_attend_pages_args {
+    int dtype;                 /* TQ_F16 or TQ_BF16: q and pools */
+    int batch, num_q_heads, num_kv_heads, head_dim;
+    int max_blocks;            /* columns of block_table */
+    int num_pages;             /* pages of the pools */
+    int selected;              /* 0: block_table [batch][max_blocks] of pages, seq_lens [batch];
+                                  1: block_table [batch][num_kv_heads][max_blocks] of head pages, seq_lens
+                                     [batch][num_kv_heads] (tq_select_pages) */
+    float scale;               /* softmax scale; 0 means 1/sqrt(head_dim) */
+    const void* q;             /* device [batch] rows of [num_q_heads][head_dim], q_stride elements apart */
+    int64_t q_stride;          /* a multiple of 8 */
+    const void* k_pool;        /* device: pages of [num_kv_heads][16][head_dim], k_page_stride elements apart */
+    const void* v_pool;
+    int64_t k_page_stride, v_page_stride;  /* multiples of 8; num_kv_heads * 16 * head_dim when selected is 1 */
+    const int32_t* block_table;/* device int32; entries past a row's length are not read */
+    const int32_t* seq_lens;   /* device int32 (clamped to 0 .. max_blocks * 16) */
+    float* out;                /* device float [batch][num_q_heads][head_dim] */
+    void* workspace;           /* device scratch (16-byte aligned); needs no initialisation, overwritten by every call */
+    size_t workspace_bytes;
+} tq_attend_pages_args;
+
+/*
+ * tq_attend_pages_workspace_bytes -- bytes of workspace tq_attend_pages needs for these shapes on the current device
+ * (never more than 8 MiB on a B200).  Only the shape fields are read.
+ */
+tq_status tq_attend_pages_workspace_bytes(const tq_attend_pages_args* args, size_t* bytes);
+
+/*
+ * tq_attend_pages -- attention of one new token per sequence over uncompressed pages: for each (b, hq), h = hq / G,
+ *   p = softmax_t(scale * q . k_t),  out = sum_t p_t v_t   over tokens 0 .. seq_lens[b] - 1.
+ * Scores, softmax and sums are fp32.  Rows of a page behind the sequence's last token may hold anything.  A sequence
+ * of length 0, or whose table entries name no page, yields zeros.  The cache is read once, in equal shares per CTA
+ * whatever the lengths; a second kernel (a programmatic dependent) joins the sequences that lie in several shares.
+ * The same inputs give the same bits on every run.  Calls that overlap on the GPU must use distinct workspaces.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8).
+ */
+tq_status tq_attend_pages(const tq_attend_pages_args* args, void* stream);
 
 /* --------------------------------------------------------------------------------------------------
  * Diagnostics.

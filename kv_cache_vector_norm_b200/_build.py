@@ -35,6 +35,22 @@ def needs_build() -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
+# source -> (its kind, the files under csrc/ it is compiled from besides tq.h and tq_internal.h)
+UNITS = {
+    "tq_lib.cu": ("cu", ("tq_device.cuh", "tq_codec_kernels.cuh", "tq_attend_kernel.cuh", "tq_qjl_kernel.cuh")),
+    "tq_pages.cu": ("cu", ("tq_device.cuh", "tq_pages_kernels.cuh")),
+    "tq_host.cpp": ("cpp", ()),
+}
+
+
+def _fresh(obj: str, src: str) -> bool:
+    """Whether an object file is newer than everything it is compiled from."""
+    if not os.path.exists(obj):
+        return False
+    deps = [os.path.join(CSRC, n) for n in (src, "tq_internal.h", *UNITS[src][1])] + [os.path.join(INCLUDE, "tq.h")]
+    return all(os.path.getmtime(d) < os.path.getmtime(obj) for d in deps)
+
+
 def nvcc() -> str:
     cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
@@ -48,8 +64,11 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     common = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", f"-I{INCLUDE}"]
     objs = []
     cmds = []
-    for src, kind in (("tq_lib.cu", "cu"), ("tq_host.cpp", "cpp")):
+    for src, (kind, _) in UNITS.items():
         obj = os.path.join(build_dir, src + ".o")
+        objs.append(obj)
+        if not force and not extra and _fresh(obj, src):
+            continue
         if kind == "cu":
             cmd = [nvcc(), *ARCH_FLAGS, *common, "-Xptxas", "-warn-spills", *extra, "-c",
                    os.path.join(CSRC, src), "-o", obj]
@@ -57,7 +76,6 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", f"-I{INCLUDE}",
                    "-I/usr/local/cuda/include", "-c", os.path.join(CSRC, src), "-o", obj]
         cmds.append(cmd)
-        objs.append(obj)
     t0 = time.time()
     procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
     for c, p in zip(cmds, procs):

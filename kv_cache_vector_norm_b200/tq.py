@@ -17,7 +17,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtq.so")
 
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_DEVICE_FLAG = range(5)
-TQ_F16, TQ_F32 = 0, 1
+TQ_F16, TQ_F32, TQ_BF16 = 0, 1, 2
 TQ_ROT_HAAR, TQ_ROT_HADAMARD = 0, 1
 ROTATIONS = {"haar": TQ_ROT_HAAR, "hadamard": TQ_ROT_HADAMARD}
 
@@ -47,6 +47,53 @@ class AttendWindow(ctypes.Structure):
 class QjlKeys(ctypes.Structure):
     """Mirror of tq_qjl_keys."""
     _fields_ = [("signs", ctypes.c_void_p), ("rho", ctypes.c_void_p)]
+
+
+class PlanArgs(ctypes.Structure):
+    """Mirror of tq_plan_args."""
+    _fields_ = [
+        ("batch", ctypes.c_int), ("num_kv_heads", ctypes.c_int), ("max_blocks", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_tokens", ctypes.c_int64), ("new_lens", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+        ("free_state", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("row_start", ctypes.c_void_p),
+        ("start_pos", ctypes.c_void_p), ("seq_lens_out", ctypes.c_void_p), ("free_state_out", ctypes.c_void_p),
+    ]
+
+
+class AppendArgs(ctypes.Structure):
+    """Mirror of tq_append_args."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("head_dim", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("num_tokens", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64), ("slots", ctypes.c_void_p), ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p), ("bounds", ctypes.c_void_p),
+    ]
+
+
+class SelectArgs(ctypes.Structure):
+    """Mirror of tq_select_args."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("num_q_heads", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("max_blocks", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("budget", ctypes.c_int), ("keep_first", ctypes.c_int),
+        ("keep_last", ctypes.c_int), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("bounds", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+    ]
+
+
+class AttendPagesArgs(ctypes.Structure):
+    """Mirror of tq_attend_pages_args."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("num_q_heads", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("max_blocks", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("selected", ctypes.c_int), ("scale", ctypes.c_float), ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("out", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
 
 
 SIGNATURES = {
@@ -94,6 +141,12 @@ SIGNATURES = {
     "tq_encode_k_qjl": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_void_p, ctypes.c_void_p]),
+    "tq_plan_pages": (ctypes.c_int, [ctypes.POINTER(PlanArgs), ctypes.c_void_p]),
+    "tq_append_pages": (ctypes.c_int, [ctypes.POINTER(AppendArgs), ctypes.c_void_p]),
+    "tq_select_pages": (ctypes.c_int, [ctypes.POINTER(SelectArgs), ctypes.c_void_p]),
+    "tq_attend_pages_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(AttendPagesArgs),
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "tq_attend_pages": (ctypes.c_int, [ctypes.POINTER(AttendPagesArgs), ctypes.c_void_p]),
 }
 
 
@@ -322,11 +375,14 @@ class Cache:
 ATTEND_WINDOW_MAX = 256
 
 
-def _window(win_k: torch.Tensor, win_v: torch.Tensor, win_lens: torch.Tensor | None, q) -> AttendWindow:
+def _window(win_k: torch.Tensor, win_v: torch.Tensor, win_lens: torch.Tensor | None, q,
+            block_table: torch.Tensor | None) -> AttendWindow:
     _need_cuda(win_k, "win_k", torch.float16)
     _need_cuda(win_v, "win_v", torch.float16)
     if win_k.dim() != 4 or win_k.shape != win_v.shape or not win_k.is_contiguous() or not win_v.is_contiguous():
         raise ValueError("win_k and win_v must be contiguous [B, H_kv, W, d] fp16 tensors of one shape")
+    if block_table is not None and block_table.dim() == 3:
+        raise ValueError("a window cannot be combined with selected pages")
     if win_k.shape[0] != q.shape[0] or win_k.shape[3] != q.shape[2]:
         raise ValueError("the window's batch and head_dim must match q")
     w = AttendWindow()
@@ -341,6 +397,14 @@ def _window(win_k: torch.Tensor, win_v: torch.Tensor, win_lens: torch.Tensor | N
 def _attend_args(codec: Codec, q, cache: Cache, *, num_kv_heads, v_bits, v_group, max_seq_len, block_table,
                  seq_lens, scale, out, workspace):
     b, hq, d = q.shape
+    if block_table is not None and block_table.dim() == 3:
+        # pages selected for each kv head (select_pages): every (sequence, kv head) is a sequence of one kv head
+        if block_table.shape[:2] != (b, num_kv_heads) or seq_lens is None or seq_lens.shape != (b, num_kv_heads):
+            raise ValueError("selected pages need block_table [B, H_kv, n] and seq_lens [B, H_kv]")
+        if hq % num_kv_heads or not (q.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous()):
+            raise ValueError("selected pages need contiguous q, block_table and seq_lens, and H_q a multiple of H_kv")
+        b, hq, num_kv_heads = b * num_kv_heads, hq // num_kv_heads, 1
+        block_table = block_table.view(b, -1)
     a = AttendArgs()
     a.batch, a.num_q_heads, a.num_kv_heads, a.head_dim = b, hq, num_kv_heads, d
     a.v_bits, a.v_group, a.scale = v_bits, v_group, float(scale)
@@ -373,7 +437,7 @@ def attend_workspace(codec: Codec, q, cache: Cache, **kw) -> torch.Tensor:
 def attend_window_workspace(codec: Codec, q, cache: Cache, win_k, win_v, win_lens=None, **kw) -> torch.Tensor:
     """A workspace of the size tq_attend_window_workspace_bytes asks for."""
     a = _attend_args(codec, q, cache, out=None, workspace=None, **kw)
-    w = _window(win_k, win_v, win_lens, q)
+    w = _window(win_k, win_v, win_lens, q, kw.get("block_table"))
     nb = ctypes.c_size_t()
     _check("tq_attend_window_workspace_bytes",
            LIB.tq_attend_window_workspace_bytes(ctypes.byref(a), ctypes.byref(w), ctypes.byref(nb)))
@@ -386,7 +450,8 @@ def attend_decode(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv_heads: 
                   workspace: torch.Tensor | None = None, win_k: torch.Tensor | None = None,
                   win_v: torch.Tensor | None = None, win_lens: torch.Tensor | None = None) -> torch.Tensor:
     """One decode step: q [B, H_q, d] fp16 against the compressed cache, plus (win_k, win_v: [B, H_kv, W, d]
-    fp16, win_lens: [B] int32 or None) a window of recent uncompressed tokens.  Returns out [B, H_q, d] f32."""
+    fp16, win_lens: [B] int32 or None) a window of recent uncompressed tokens.  Returns out [B, H_q, d] f32.
+    block_table [B, H_kv, n] with seq_lens [B, H_kv] (select_pages) attends to the selected pages of a paged cache."""
     _need_cuda(q, "q", torch.float16)
     kw = dict(num_kv_heads=num_kv_heads, v_bits=v_bits, v_group=v_group, max_seq_len=max_seq_len,
               block_table=block_table, seq_lens=seq_lens, scale=scale)
@@ -401,7 +466,7 @@ def attend_decode(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv_heads: 
     if workspace is None:
         workspace = attend_window_workspace(codec, q, cache, win_k, win_v, win_lens, **kw)
     a = _attend_args(codec, q, cache, out=out, workspace=workspace, **kw)
-    w = _window(win_k, win_v, win_lens, q)
+    w = _window(win_k, win_v, win_lens, q, block_table)
     _check("tq_attend_decode_window", LIB.tq_attend_decode_window(codec.handle, ctypes.byref(a), ctypes.byref(w),
                                                                   _stream(q.device)))
     return out
@@ -416,7 +481,7 @@ def attend_scores(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv_heads: 
     _need_cuda(q, "q", torch.float16)
     kw = dict(num_kv_heads=num_kv_heads, v_bits=v_bits, v_group=v_group, max_seq_len=max_seq_len,
               block_table=block_table, seq_lens=seq_lens, scale=scale)
-    length = block_table.shape[1] * 16 if block_table is not None else int(max_seq_len)
+    length = block_table.shape[-1] * 16 if block_table is not None else int(max_seq_len)
     scores = torch.empty((q.shape[0], q.shape[1], length), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = attend_workspace(codec, q, cache, **kw)
@@ -469,6 +534,204 @@ def attend_decode_noalloc(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv
                      max_seq_len=max_seq_len, block_table=block_table, seq_lens=seq_lens, scale=scale, out=out,
                      workspace=None)
     _check("tq_attend_decode_noalloc", LIB.tq_attend_decode_noalloc(codec.handle, ctypes.byref(a), _stream(q.device)))
+    return out
+
+
+# ---------------------------------------------------------------------------------- the paged cache
+
+PAGE = 16                                               # tokens per page
+_PAGE_DTYPES = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+
+
+def _page_dtype(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _PAGE_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _need(t: torch.Tensor, name: str, dtype, shape, device):
+    """Pointer of a contiguous tensor of this dtype, shape (None: any extent) and device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if t.dim() != len(shape) or any(w is not None and w != s for s, w in zip(t.shape, shape)) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {list(shape)} (None: any), got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _run_on(device: torch.device, name: str, args):
+    """Enqueue a call on the current stream of `device`, whichever device is current."""
+    if device.index == torch.cuda.current_device():
+        _check(name, getattr(LIB, name)(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(name, getattr(LIB, name)(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream))
+
+
+@dataclass
+class PagePlan:
+    """One step's plan (tq_plan_pages): where each input row goes, and the requests' state after the step."""
+    slots: torch.Tensor          # int64 [max_tokens * H_kv], -1 for rows that are not stored
+    row_start: torch.Tensor      # int32 [B + 1]
+    start_pos: torch.Tensor      # int32 [B], -1: refused or finished
+    seq_lens: torch.Tensor       # int32 [B]
+    free_state: torch.Tensor     # int32 [2]
+
+
+def plan_pages(new_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+               free_state: torch.Tensor, *, num_kv_heads: int, max_tokens: int | None = None,
+               slots: torch.Tensor | None = None, row_start: torch.Tensor | None = None,
+               start_pos: torch.Tensor | None = None, seq_lens_out: torch.Tensor | None = None,
+               free_state_out: torch.Tensor | None = None) -> PagePlan:
+    """Pages and slots for one step's new tokens.  new_lens, seq_lens: int32 [B]; block_table: int32 [B, max_blocks]
+    and free_pages: int32 [num_pages] (a ring; free_state: int32 [first, count]) are updated in place.  max_tokens:
+    input rows the caller has (or slots of that many rows).  seq_lens_out / free_state_out may be seq_lens /
+    free_state themselves."""
+    if not isinstance(new_lens, torch.Tensor) or not new_lens.is_cuda:
+        raise TypeError("new_lens must be a CUDA tensor")
+    dev, b = new_lens.device, new_lens.shape[0]
+    if slots is None:
+        if max_tokens is None:
+            raise ValueError("plan_pages needs max_tokens or slots")
+        slots = torch.empty(max_tokens * num_kv_heads, dtype=torch.int64, device=dev)
+    elif max_tokens is None:
+        max_tokens = slots.numel() // num_kv_heads
+    if row_start is None:
+        row_start = torch.empty(b + 1, dtype=torch.int32, device=dev)
+    if start_pos is None:
+        start_pos = torch.empty(b, dtype=torch.int32, device=dev)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
+    if free_state_out is None:
+        free_state_out = torch.empty(2, dtype=torch.int32, device=dev)
+    i32 = torch.int32
+    a = PlanArgs(b, num_kv_heads, block_table.shape[-1], free_pages.shape[0], max_tokens,
+                 _need(new_lens, "new_lens", i32, (b,), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
+                 _need(block_table, "block_table", i32, (b, None), dev),
+                 _need(free_pages, "free_pages", i32, (None,), dev), _need(free_state, "free_state", i32, (2,), dev),
+                 _need(slots, "slots", torch.int64, (max_tokens * num_kv_heads,), dev),
+                 _need(row_start, "row_start", i32, (b + 1,), dev), _need(start_pos, "start_pos", i32, (b,), dev),
+                 _need(seq_lens_out, "seq_lens_out", i32, (b,), dev),
+                 _need(free_state_out, "free_state_out", i32, (2,), dev))
+    _run_on(dev, "tq_plan_pages", a)
+    return PagePlan(slots, row_start, start_pos, seq_lens_out, free_state_out)
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor):
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [N, H_kv, d] like k, with unit stride along d")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def append_pages(k: torch.Tensor, v: torch.Tensor | None, slots: torch.Tensor, *, k_pool: torch.Tensor | None = None,
+                 v_pool: torch.Tensor | None = None, bounds: torch.Tensor | None = None) -> None:
+    """Store k, v [N, H_kv, d] (fp16 or bf16; strided views of a fused projection are fine) at slots int64 [N * H_kv]
+    of k_pool, v_pool [num_pages, H_kv, 16, d], and keep bounds [num_pages, H_kv, 2, d], the lowest and highest key of
+    every page and channel.  Any of the three may be left out (bounds alone for a compressed cache)."""
+    dtype = _page_dtype(k, "k")
+    if k.dim() != 3:
+        raise ValueError("k must be [N, H_kv, d]")
+    n, h, d = k.shape
+    dev = k.device
+    pages = next((t.shape[0] for t in (k_pool, v_pool, bounds) if t is not None), 0)
+    if v_pool is not None and v is None:
+        raise ValueError("v_pool needs v")
+    kp, k_tok, k_head = _rows(k, "k", k)
+    vp, v_tok, v_head = _rows(v, "v", k) if v is not None else (None, 0, 0)
+    a = AppendArgs(dtype, d, h, pages, n, kp, vp, k_tok, k_head, v_tok, v_head,
+                   _need(slots, "slots", torch.int64, (n * h,), dev),
+                   _need(k_pool, "k_pool", k.dtype, (pages, h, PAGE, d), dev) if k_pool is not None else None,
+                   _need(v_pool, "v_pool", k.dtype, (pages, h, PAGE, d), dev) if v_pool is not None else None,
+                   _need(bounds, "bounds", k.dtype, (pages, h, 2, d), dev) if bounds is not None else None)
+    _run_on(dev, "tq_append_pages", a)
+
+
+def _q_rows(q: torch.Tensor):
+    """dtype code, sizes and batch stride of a query [B, H_q, d] whose sequences may lie apart."""
+    dtype = _page_dtype(q, "q")
+    if q.dim() != 3 or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
+        raise ValueError("q must be [B, H_q, d] with contiguous heads")
+    return dtype, *q.shape, q.stride(0)
+
+
+def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *, budget: int,
+                 keep_first: int = 1, keep_last: int = 1, pages: torch.Tensor | None = None,
+                 lens: torch.Tensor | None = None):
+    """The `budget` pages of each (sequence, kv head) whose bounds allow the largest q . k (the first keep_first and
+    last keep_last always): (pages int32 [B, H_kv, budget] of head pages, lens int32 [B, H_kv]), to be passed as
+    block_table and seq_lens to attend_pages or attend_decode."""
+    dtype, b, hq, d, q_stride = _q_rows(q)
+    dev = q.device
+    if bounds.dim() != 4:
+        raise ValueError("bounds must be [num_pages, H_kv, 2, d]")
+    n, h = bounds.shape[:2]
+    if pages is None:
+        pages = torch.empty((b, h, budget), dtype=torch.int32, device=dev)
+    if lens is None:
+        lens = torch.empty((b, h), dtype=torch.int32, device=dev)
+    i32 = torch.int32
+    a = SelectArgs(dtype, b, hq, h, d, block_table.shape[-1], n, budget, keep_first, keep_last, q.data_ptr(), q_stride,
+                   _need(bounds, "bounds", q.dtype, (n, h, 2, d), dev),
+                   _need(block_table, "block_table", i32, (b, None), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
+                   _need(pages, "pages", i32, (b, h, budget), dev), _need(lens, "lens", i32, (b, h), dev))
+    _run_on(dev, "tq_select_pages", a)
+    return pages, lens
+
+
+def _pool(t: torch.Tensor, name: str, shape, q):
+    """Pointer and page stride of a pool whose pages are contiguous but may lie apart (a half of a joint pool)."""
+    if t.dtype != q.dtype or t.device != q.device or t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} with the dtype and device of q")
+    if t.stride()[1:] != (PAGE * shape[3], shape[3], 1):
+        raise ValueError(f"each page of {name} must be contiguous [H_kv, 16, d]")
+    return t.data_ptr(), t.stride(0)
+
+
+def _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace) -> AttendPagesArgs:
+    dtype, b, hq, d, q_stride = _q_rows(q)
+    dev = q.device
+    if k_pool.dim() != 4 or k_pool.shape[2:] != (PAGE, d):
+        raise ValueError("k_pool must be [num_pages, H_kv, 16, d]")
+    n, h = k_pool.shape[:2]
+    kp, k_page = _pool(k_pool, "k_pool", k_pool.shape, q)
+    vp, v_page = _pool(v_pool, "v_pool", k_pool.shape, q)
+    selected = block_table.dim() == 3
+    rows = (b, h) if selected else (b,)
+    return AttendPagesArgs(dtype, b, hq, h, d, block_table.shape[-1], n, int(selected), float(scale), q.data_ptr(),
+                           q_stride, kp, vp, k_page, v_page,
+                           _need(block_table, "block_table", torch.int32, (*rows, None), dev),
+                           _need(seq_lens, "seq_lens", torch.int32, rows, dev),
+                           _need(out, "out", torch.float32, (b, hq, d), dev) if out is not None else None,
+                           workspace.data_ptr() if workspace is not None else None,
+                           workspace.numel() * workspace.element_size() if workspace is not None else 0)
+
+
+def attend_pages_workspace(q, k_pool, v_pool, block_table, seq_lens) -> torch.Tensor:
+    """A workspace of the size tq_attend_pages_workspace_bytes asks for."""
+    a = _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, 0.0, None, None)
+    nb = ctypes.c_size_t()
+    with torch.cuda.device(q.device):
+        _check("tq_attend_pages_workspace_bytes",
+               LIB.tq_attend_pages_workspace_bytes(ctypes.byref(a), ctypes.byref(nb)))
+    return torch.empty(nb.value, dtype=torch.uint8, device=q.device)
+
+
+def attend_pages(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, *, scale: float = 0.0, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """One decode step over uncompressed pages: q [B, H_q, d] (fp16 or bf16) against k_pool, v_pool [num_pages, H_kv,
+    16, d], with block_table int32 [B, max_blocks] and seq_lens int32 [B], or the pages of a selection: block_table
+    [B, H_kv, n] and seq_lens [B, H_kv] (select_pages).  Returns out [B, H_q, d] f32."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = attend_pages_workspace(q, k_pool, v_pool, block_table, seq_lens)
+    elif workspace.device != q.device:
+        raise TypeError(f"workspace must be on {q.device}")
+    _run_on(q.device, "tq_attend_pages",
+            _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace))
     return out
 
 
