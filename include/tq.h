@@ -514,7 +514,17 @@ typedef struct tq_select_args {
     const int32_t* seq_lens;   /* device [batch] (clamped to 0 .. max_blocks * 16) */
     int32_t* pages;            /* out, device [batch][num_kv_heads][budget]: head pages in ascending order, then -1 */
     int32_t* lens;             /* out, device [batch][num_kv_heads]: tokens of the listed pages */
+    void* workspace;           /* device scratch (4-byte aligned; may be NULL if none is needed): the scores of a call
+                                  with few rows; needs no initialisation, overwritten by every call that uses it */
+    size_t workspace_bytes;
 } tq_select_args;
+
+/*
+ * tq_select_pages_workspace_bytes -- bytes of workspace tq_select_pages needs for these shapes on the current device:
+ * 0, or 4 * batch * num_kv_heads * max_blocks when there are fewer (sequence, kv head) rows than SMs or rows are very
+ * long.  Only the shape fields are read.
+ */
+tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* bytes);
 
 /*
  * tq_select_pages -- the pages a decode step attends to.  For each page of a sequence and each kv head,
@@ -527,7 +537,8 @@ typedef struct tq_select_args {
  * of one kv head: a head page is a page of a pool with one kv head.
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
  * result is the same on every run and for every shape of the call.  A score that is not a number ranks last.
- * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8, max_blocks too large).
+ * Calls that overlap on the GPU must use distinct workspaces.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8, 2^39 pages or more in all rows).
  */
 tq_status tq_select_pages(const tq_select_args* args, void* stream);
 

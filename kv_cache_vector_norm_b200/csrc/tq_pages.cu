@@ -44,7 +44,7 @@ int device_sms() {
 
 // Function attributes are set once per device and kernel.
 template <auto Kernel>
-cudaError_t prepare_kernel(int smem, bool wide_clusters) {
+cudaError_t prepare_kernel(int smem) {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -52,7 +52,6 @@ cudaError_t prepare_kernel(int smem, bool wide_clusters) {
     const uint64_t bit = 1ull << (dev & 63);
     if (done.load() & bit) return cudaSuccess;
     e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && wide_clusters) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) done.fetch_or(bit);
     return e;
 }
@@ -128,7 +127,10 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // a decode step's few slots are written by the planning CTA itself, a prefill's by a grid of their own
     const bool one = a->max_tokens <= 1024;
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(p, one);
+    if (a->batch <= 256 && one)
+        plan_kernel<256><<<1, 256, 0, st>>>(p, one);
+    else
+        plan_kernel<kPlanThreads><<<1, kPlanThreads, 0, st>>>(p, one);
     TQ_CUDA(cudaGetLastError(), "tq_plan_pages: launch");
     if (!one) {
         cudaLaunchAttribute attr[1];
@@ -152,7 +154,11 @@ namespace {
 template <typename T, int D>
 tq_status launch_append(const AppendParams& p, cudaStream_t st) {
     const int64_t warps = (p.n + p.tile - 1) / p.tile * p.heads;
-    append_kernel<T, D><<<static_cast<unsigned>((warps + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, st>>>(p);
+    const unsigned grid = static_cast<unsigned>((warps + kAppendWarps - 1) / kAppendWarps);
+    if (p.v_pool)
+        append_kernel<T, D, true><<<grid, 32 * kAppendWarps, 0, st>>>(p);
+    else
+        append_kernel<T, D, false><<<grid, 32 * kAppendWarps, 0, st>>>(p);
     TQ_CUDA(cudaGetLastError(), "tq_append_pages: launch");
     return TQ_OK;
 }
@@ -205,43 +211,15 @@ extern "C" tq_status tq_append_pages(const tq_append_args* a, void* stream) {
 namespace {
 
 constexpr int kSelSmem = 200 << 10;
-constexpr int kMaxCluster = 16;
+constexpr int kSortRoom = 32768;       // keys that select_kernel's SCORED form keeps in shared memory
 
-template <typename T, int D>
-tq_status launch_select(SelectParams& p, int batch, cudaStream_t st) {
-    constexpr auto kern = select_kernel<T, D>;
-    TQ_CUDA((prepare_kernel<kern>(kSelSmem, true)), "tq_select_pages: cudaFuncSetAttribute");
-    const int64_t rows = static_cast<int64_t>(batch) * p.heads;
-    const int cap = static_cast<int>((kSelSmem - select_smem(0, p.group, D)) / 8);
-    // enough CTAs per row to cover the SMs, but at least 64 pages each, and as many as its pages need to fit
-    int cs = 1;
-    while (cs < kMaxCluster && (rows * cs < device_sms() && p.width / (2 * cs) >= 64)) cs *= 2;
-    while (cs < kMaxCluster && (p.width + cs - 1) / cs > cap) cs *= 2;
-    p.share_cap = (p.width + cs - 1) / cs;
-    TQ_NEED(p.share_cap <= cap && p.share_cap < 65536, TQ_ERR_UNSUPPORTED, "tq_select_pages: max_blocks=%d (at most %d)", p.width,
-            kMaxCluster * cap);
-    TQ_NEED(rows * cs < (1ll << 31), TQ_ERR_UNSUPPORTED, "tq_select_pages: too many rows");
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cs;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * cs));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = select_smem(p.share_cap, p.group, D);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    TQ_CUDA(cudaLaunchKernelEx(&cfg, kern, p), "tq_select_pages: launch");
-    return TQ_OK;
-}
+struct SelectPlan {
+    bool scored;                       // the keys are computed by a grid of their own, through the workspace
+    int room;                          // pages whose keys select_kernel keeps in shared memory
+    size_t workspace_bytes;
+};
 
-}  // namespace
-
-extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
-    clear_error();
-    const char* fn = "tq_select_pages";
+tq_status plan_select(const char* fn, const tq_select_args* a, SelectPlan* plan) {
     TQ_NEED(a, TQ_ERR_INVALID_ARG, "%s: args is NULL", fn);
     tq_status s = check_heads(fn, a->batch, a->num_q_heads, a->num_kv_heads);
     if (s != TQ_OK) return s;
@@ -252,11 +230,75 @@ extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
                 a->keep_last <= a->budget - a->keep_first,
             TQ_ERR_INVALID_ARG, "%s: budget=%d must hold keep_first=%d (>= 0) and keep_last=%d (>= 1) pages", fn, a->budget,
             a->keep_first, a->keep_last);
+    const int64_t rows = static_cast<int64_t>(a->batch) * a->num_kv_heads;
+    const int width = a->max_blocks, even = (width + 1) & ~1;
+    // With fewer rows than SMs the scores take a grid over all pages; with many rows, or with few pages, a second
+    // kernel costs more than it brings, unless a row's keys and page ids do not fit one CTA's shared memory.
+    const bool fits = query_smem(a->num_q_heads / a->num_kv_heads, a->head_dim) + static_cast<size_t>(even) * 8 <= kSelSmem;
+    plan->scored = !fits || (rows < device_sms() && width > kScoreTile);
+    plan->room = plan->scored ? (width < kSortRoom ? width : kSortRoom) : even;
+    TQ_NEED(rows * ((width + kScoreTile - 1) / kScoreTile) < (1ll << 31), TQ_ERR_UNSUPPORTED,
+            "%s: too many (sequence, kv head) rows for max_blocks=%d", fn, width);
+    plan->workspace_bytes = plan->scored ? static_cast<size_t>(rows) * width * 4 : 0;
+    return TQ_OK;
+}
+
+template <typename T, int D>
+tq_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>(rows);
+    if (!scored) {
+        constexpr auto kern = select_kernel<T, D, false>;
+        TQ_CUDA((prepare_kernel<kern>(kSelSmem)), "tq_select_pages: cudaFuncSetAttribute");
+        kern<<<grid, kScoreThreads, query_smem(p.group, D) + static_cast<size_t>(p.room) * 8, st>>>(p);
+        TQ_CUDA(cudaGetLastError(), "tq_select_pages: launch");
+        return TQ_OK;
+    }
+    // the selection itself does not depend on the type or the head size
+    constexpr auto kern = select_kernel<__half, 64, true>;
+    TQ_CUDA((prepare_kernel<kern>(kSortRoom * 4)), "tq_select_pages: cudaFuncSetAttribute");
+    const unsigned tiles = (p.width + kScoreTile - 1) / kScoreTile;
+    score_kernel<T, D><<<grid * tiles, kScoreThreads, query_smem(p.group, D), st>>>(p);
+    TQ_CUDA(cudaGetLastError(), "tq_select_pages: score launch");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.room) * 4;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    TQ_CUDA(cudaLaunchKernelEx(&cfg, kern, p), "tq_select_pages: launch");
+    return TQ_OK;
+}
+
+}  // namespace
+
+extern "C" tq_status tq_select_pages_workspace_bytes(const tq_select_args* a, size_t* bytes) {
+    clear_error();
+    TQ_NEED(bytes, TQ_ERR_INVALID_ARG, "tq_select_pages_workspace_bytes: bytes is NULL");
+    *bytes = 0;
+    SelectPlan plan;
+    tq_status s = plan_select("tq_select_pages_workspace_bytes", a, &plan);
+    if (s != TQ_OK) return s;
+    *bytes = plan.workspace_bytes;
+    return TQ_OK;
+}
+
+extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
+    clear_error();
+    const char* fn = "tq_select_pages";
+    SelectPlan plan;
+    tq_status s = plan_select(fn, a, &plan);
+    if (s != TQ_OK) return s;
     TQ_NEED(a->q && a->bounds && a->block_table && a->seq_lens && a->pages && a->lens, TQ_ERR_INVALID_ARG, "%s: NULL pointer in args", fn);
+    TQ_NEED(plan.workspace_bytes == 0 || (a->workspace && a->workspace_bytes >= plan.workspace_bytes), TQ_ERR_INVALID_ARG,
+            "%s: workspace of %zu bytes required (got %zu)", fn, plan.workspace_bytes, a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
     TQ_NEED(aligned(a->q, 16) && aligned(a->bounds, 16), TQ_ERR_INVALID_ARG, "%s: q and bounds must be 16-byte aligned", fn);
     TQ_NEED(a->q_stride % 8 == 0 && a->q_stride >= 0, TQ_ERR_INVALID_ARG, "%s: q_stride must be a non-negative multiple of 8", fn);
-    TQ_NEED(aligned(a->block_table, 4) && aligned(a->seq_lens, 4) && aligned(a->pages, 4) && aligned(a->lens, 4), TQ_ERR_INVALID_ARG,
-            "%s: misaligned pointer in args", fn);
+    TQ_NEED(aligned(a->block_table, 4) && aligned(a->seq_lens, 4) && aligned(a->pages, 4) && aligned(a->lens, 4) && aligned(a->workspace, 4),
+            TQ_ERR_INVALID_ARG, "%s: misaligned pointer in args", fn);
     SelectParams p;
     p.q = a->q;
     p.q_stride = a->q_stride;
@@ -272,19 +314,23 @@ extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
     p.budget = a->budget;
     p.keep_first = a->keep_first;
     p.keep_last = a->keep_last;
-    p.share_cap = 0;
+    p.room = plan.room;
+    p.keys = static_cast<uint32_t*>(a->workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_select, p, a->batch, st);
+    const int64_t rows = static_cast<int64_t>(a->batch) * a->num_kv_heads;
+    TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_select, p, rows, plan.scored, st);
 }
 
 // -------------------------------------------------------------------------------------------- attend
 
 namespace {
 
-constexpr int kMinPages = 4;           // pages a CTA takes at least: one per warp
+// A share is at least a row's own cost and a page for each warp.
+template <int D>
+constexpr int min_share() { return PagesCfg<D>::kRowCost + PagesCfg<D>::kWarps; }
 
 struct PagesPlan {
-    int ctas;
+    int ctas, rows_join;
     size_t meta_bytes, workspace_bytes;
 };
 
@@ -296,29 +342,39 @@ tq_status plan_attend_pages(const char* fn, const tq_attend_pages_args* a, Pages
     if ((s = check_pool(fn, a->num_pages, a->num_kv_heads)) != TQ_OK) return s;
     TQ_NEED(a->max_blocks >= 1 && a->max_blocks <= (1 << 26), TQ_ERR_INVALID_ARG, "%s: max_blocks=%d outside 1 .. 2^26", fn, a->max_blocks);
     TQ_NEED(a->selected == 0 || a->selected == 1, TQ_ERR_INVALID_ARG, "%s: selected=%d (0 or 1)", fn, a->selected);
-    const int64_t pages = static_cast<int64_t>(a->batch) * a->num_kv_heads * a->max_blocks;   // at most
-    const int64_t slots = static_cast<int64_t>(device_sms()) * (a->head_dim == 256 ? PagesCfg<256>::kCtasPerSm : PagesCfg<128>::kCtasPerSm);
-    const int64_t want = (pages + kMinPages - 1) / kMinPages;
+    const int d = a->head_dim;
+    const int row_cost = d == 64 ? PagesCfg<64>::kRowCost : d == 128 ? PagesCfg<128>::kRowCost : PagesCfg<256>::kRowCost;
+    const int per_sm = d == 64 ? PagesCfg<64>::kCtasPerSm : d == 128 ? PagesCfg<128>::kCtasPerSm : PagesCfg<256>::kCtasPerSm;
+    const int least = d == 64 ? min_share<64>() : d == 128 ? min_share<128>() : min_share<256>();
+    const int64_t cost = static_cast<int64_t>(a->batch) * a->num_kv_heads * (a->max_blocks + row_cost);   // at most
+    const int64_t slots = static_cast<int64_t>(device_sms()) * per_sm;
+    const int64_t want = (cost + least - 1) / least;
+    TQ_NEED(cost < (1ll << 31), TQ_ERR_UNSUPPORTED, "%s: batch=%d with %d kv heads and max_blocks=%d holds 2^31 pages or more", fn,
+            a->batch, a->num_kv_heads, a->max_blocks);
     plan->ctas = static_cast<int>(want < slots ? want : slots);
+    // the join goes by rows if there are no more of them than shares
+    const int rows = a->batch * a->num_kv_heads;
+    plan->rows_join = rows <= plan->ctas ? rows : 0;
     plan->meta_bytes = static_cast<size_t>(plan->ctas) * sizeof(AttendPagesMeta);
-    plan->workspace_bytes = plan->meta_bytes + static_cast<size_t>(plan->ctas) * 2 * (16 + 8 * a->head_dim) * 4;
+    plan->workspace_bytes = plan->meta_bytes + static_cast<size_t>(plan->ctas) * 2 * (16 + 8 * d) * 4;
     return TQ_OK;
 }
 
 template <typename T, int D>
-tq_status launch_attend_pages(const AttendPagesParams& p, int ctas, cudaStream_t st) {
+tq_status launch_attend_pages(AttendPagesParams& p, int ctas, cudaStream_t st) {
     using C = PagesCfg<D>;
+    p.min_share = min_share<D>();
     constexpr auto kern = attend_pages_kernel<T, D>;
-    TQ_CUDA((prepare_kernel<kern>(C::kSmem, false)), "tq_attend_pages: cudaFuncSetAttribute");
-    kern<<<ctas, C::kThreads, C::kSmem, st>>>(p);
+    TQ_CUDA((prepare_kernel<kern>(C::smem(8))), "tq_attend_pages: cudaFuncSetAttribute");
+    kern<<<ctas, C::kThreads, C::smem(p.group), st>>>(p);
     TQ_CUDA(cudaGetLastError(), "tq_attend_pages: launch");
     if (ctas > 1) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(ctas - 1, p.group);
-        cfg.blockDim = dim3(kJoinThreads);
+        cfg.gridDim = dim3(p.rows_join ? p.rows_join : ctas - 1, (p.group + p.join_heads - 1) / p.join_heads);
+        cfg.blockDim = dim3(p.rows_join ? kJoinThreads : p.join_heads * D);   // going by shares: four slices
         cfg.stream = st;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -371,7 +427,6 @@ extern "C" tq_status tq_attend_pages(const tq_attend_pages_args* a, void* stream
     p.heads = a->num_kv_heads;
     p.group = a->num_q_heads / a->num_kv_heads;
     p.width = a->max_blocks;
-    p.min_pages = kMinPages;
     const float scale = (a->scale == 0.f) ? 1.0f / std::sqrt(static_cast<float>(a->head_dim)) : a->scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     if (a->selected) {                 // a table row per (sequence, kv head) of head pages
@@ -386,6 +441,16 @@ extern "C" tq_status tq_attend_pages(const tq_attend_pages_args* a, void* stream
         p.k_page = a->k_page_stride;
         p.v_page = a->v_page_stride;
     }
+    p.rows_join = plan.rows_join;
+    // rows in many shares are joined by a CTA per head (or per few, so that the CTAs are resident together), those in
+    // the few shares that many rows have by a CTA for 64 threads' worth of heads
+    p.join_heads = 256 / a->head_dim;
+    if (plan.rows_join) {
+        p.join_heads = 1;
+        while (p.join_heads < p.group && p.rows_join * ((p.group + p.join_heads - 1) / p.join_heads) > device_sms()) ++p.join_heads;
+    }
+    if (p.join_heads > p.group) p.join_heads = p.group;
+    if (p.join_heads * a->head_dim / 4 > kJoinThreads) p.join_heads = kJoinThreads * 4 / a->head_dim;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_attend_pages, p, plan.ctas, st);
 }

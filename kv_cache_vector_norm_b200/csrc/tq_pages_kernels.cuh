@@ -31,12 +31,15 @@ struct PlanParams {
     int64_t max_tokens;
 };
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;      // requests a CTA of plan_kernel plans at a time, at most
 constexpr int kSlotTile = 256;         // tokens whose slots one CTA of plan_slots_kernel writes
+constexpr int kSlotBatch = 2048;       // row starts it keeps in shared memory
 
 // Inclusive scan of two values over the block (every thread takes part); `total` receives the block's sums.
+template <int NT>
 __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t (&total)[2], int64_t (*warp_sums)[2]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    constexpr int NW = NT / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t ta = __shfl_up_sync(0xffffffffu, a, o), tb = __shfl_up_sync(0xffffffffu, b, o);
@@ -45,58 +48,37 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t (&to
     __syncthreads();                                     // warp_sums may still be read from the scan before
     if (lane == 31) { warp_sums[warp][0] = a; warp_sums[warp][1] = b; }
     __syncthreads();
-    if (warp == 0) {
-        int64_t sa = lane < nwarps ? warp_sums[lane][0] : 0, sb = lane < nwarps ? warp_sums[lane][1] : 0;
+    // every warp adds up the warps before it
+    int64_t sa = lane < NW ? warp_sums[lane][0] : 0, sb = lane < NW ? warp_sums[lane][1] : 0;
+    int64_t ba = lane < warp ? sa : 0, bb = lane < warp ? sb : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t ta = __shfl_up_sync(0xffffffffu, sa, o), tb = __shfl_up_sync(0xffffffffu, sb, o);
-            if (lane >= o) { sa += ta; sb += tb; }
-        }
-        if (lane < nwarps) { warp_sums[lane][0] = sa; warp_sums[lane][1] = sb; }
+    for (int o = (NW > 16 ? 16 : NW / 2); o; o >>= 1) {
+        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        sb += __shfl_xor_sync(0xffffffffu, sb, o);
+        ba += __shfl_xor_sync(0xffffffffu, ba, o);
+        bb += __shfl_xor_sync(0xffffffffu, bb, o);
     }
-    __syncthreads();
-    if (warp > 0) { a += warp_sums[warp - 1][0]; b += warp_sums[warp - 1][1]; }
-    total[0] = warp_sums[nwarps - 1][0];
-    total[1] = warp_sums[nwarps - 1][1];
+    a += __shfl_sync(0xffffffffu, ba, 0);
+    b += __shfl_sync(0xffffffffu, bb, 0);
+    total[0] = __shfl_sync(0xffffffffu, sa, 0);
+    total[1] = __shfl_sync(0xffffffffu, sb, 0);
 }
 
-// The slot of kv head 0 of input row `token`, or -1: rows of refused or finished requests, rows past the last
-// request's, and tokens whose table entry names no page.
-__device__ __forceinline__ int64_t plan_slot(const PlanParams& p, int64_t token) {
-    int lo = 0, hi = p.batch;                            // the first request whose rows end after `token`
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.row_start[mid + 1] <= token) lo = mid + 1; else hi = mid;
-    }
-    if (lo == p.batch) return -1;
-    const int start = p.start_pos[lo];
-    if (start < 0) return -1;
-    const int64_t pos = start + (token - p.row_start[lo]);
-    const int page = p.table[static_cast<int64_t>(lo) * p.width + pos / kPage];
-    if (page < 0 || page >= p.num_pages) return -1;
-    return static_cast<int64_t>(page) * p.heads * kPage + pos % kPage;
+// The slot of kv head 0 of a page's row, -1 if the id names no page.
+__device__ __forceinline__ int64_t page_slot(const PlanParams& p, int page, int64_t pos) {
+    return (page < 0 || page >= p.num_pages) ? -1 : static_cast<int64_t>(page) * p.heads * kPage + pos % kPage;
 }
 
-// Slots of `n` tokens from `token0` on: one search per token, then the tokens' H_kv slots with coalesced stores.
-__device__ __forceinline__ void write_slots(const PlanParams& p, int64_t token0, int n, int64_t* base) {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) base[i] = plan_slot(p, token0 + i);
-    __syncthreads();
-    int64_t* dst = p.slots + token0 * p.heads;
-    for (int i = threadIdx.x; i < n * p.heads; i += blockDim.x) {
-        const int t = i / p.heads, h = i - t * p.heads;
-        dst[i] = base[t] < 0 ? -1 : base[t] + h * kPage;
-    }
-}
-
-// One CTA: lengths, admission, table rows and the free ring.  Admission is a prefix rule (a request that needs
-// pages gets them when the running sum of needs up to it is within the free count), so two scans decide it for
-// every request at once.  Pages are taken from the ring's start and given back at its end, so what this call reads
-// and what it writes never overlap.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, bool with_slots) {
-    __shared__ int64_t s_warp[32][2];
-    __shared__ int64_t s_base[kPlanThreads];
-    __shared__ int s_old[kPlanThreads], s_need[kPlanThreads], s_from[kPlanThreads], s_gone[kPlanThreads],
-        s_to[kPlanThreads];
+// One CTA: lengths, admission, table rows and the free ring; with_slots: the slots too.  Admission is a prefix rule (a
+// request that needs pages gets them when the running sum of needs up to it is within the free count), so two scans
+// decide it for every request at once.  Pages are taken from the ring's start and given back at its end, so what this
+// call reads and what it writes never overlap, and a request's slots follow from its table row as it was and from its
+// part of the ring, without waiting for the table.
+template <int NT>
+__global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_slots) {
+    __shared__ int64_t s_warp[NT / 32][2];
+    __shared__ int s_len[NT], s_need[NT], s_from[NT], s_gone[NT], s_to[NT], s_req[NT];
+    __shared__ int64_t s_row[NT];
     __shared__ int s_taken;
     // the slot grid (a programmatic dependent) may be scheduled; it waits for this grid's completion
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -111,7 +93,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         p.row_start[0] = 0;
     }
     int64_t rows_before = 0, gone_before = 0, need_before = 0, total[2];
-    for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < p.batch; b0 += NT) {
         const int b = b0 + tid;
         const bool active = b < p.batch;
         const int want = active ? p.new_lens[b] : 0;
@@ -121,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         const int64_t old_pages = (len + kPage - 1) / kPage;
         const int64_t gone = want < 0 ? old_pages : 0;
         int64_t end = req, gone_end = gone;
-        block_scan2(end, gone_end, total, s_warp);
+        block_scan2<NT>(end, gone_end, total, s_warp);
         end += rows_before;
         gone_end += gone_before;
         rows_before += total[0];
@@ -129,7 +111,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         const bool fits = active && want >= 0 && len + req <= most && end <= p.max_tokens;
         const int64_t need = fits ? (len + req + kPage - 1) / kPage - old_pages : 0;
         int64_t upto = need, unused = 0;
-        block_scan2(upto, unused, total, s_warp);
+        block_scan2<NT>(upto, unused, total, s_warp);
         upto += need_before;
         need_before += total[0];
         const bool ok = fits && (need == 0 || upto <= count);
@@ -140,34 +122,53 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
             p.seq_lens_out[b] = want < 0 ? 0 : static_cast<int>(len + (ok ? req : 0));
         }
         const int64_t to = gone_end - gone;
-        s_old[tid] = static_cast<int>(old_pages);
+        s_len[tid] = ok ? static_cast<int>(len) : ~static_cast<int>(old_pages);     // refused: the pages it has
         s_need[tid] = ok ? static_cast<int>(need) : 0;
         s_from[tid] = ok ? static_cast<int>(upto - need) : 0;
         s_gone[tid] = static_cast<int>(gone);
         s_to[tid] = to > cap ? cap : static_cast<int>(to);
+        s_req[tid] = static_cast<int>(req);
+        s_row[tid] = end - req;
         __syncthreads();
-        // table rows and the ring: the block's threads in equal groups, a request per group
-        const int n = p.batch - b0 < kPlanThreads ? p.batch - b0 : kPlanThreads;
-        int per = kPlanThreads;
-        while (per > 32 && per * n > kPlanThreads) per >>= 1;
+        // table rows, ring and slots: the block's threads in equal groups, a request per group
+        const int n = p.batch - b0 < NT ? p.batch - b0 : NT;
+        int per = NT;
+        while (per > 1 && per * n > NT) per >>= 1;
         const int lane = tid & (per - 1);
-        for (int i = tid / per; i < n; i += kPlanThreads / per) {
+        for (int i = tid / per; i < n; i += NT / per) {
             int32_t* row = p.table + static_cast<int64_t>(b0 + i) * p.width;
-            const int need_i = s_need[i], gone_i = s_gone[i];
-            int32_t* fresh = row + s_old[i];
+            const int need_i = s_need[i], gone_i = s_gone[i], len_i = s_len[i];
+            const int old = len_i < 0 ? ~len_i : (len_i + kPage - 1) / kPage;
             const int from = head + s_from[i];           // below 2 cap: from + j - head < count <= cap
+            auto fresh = [&](int j) { return p.ring[from + j >= cap ? from + j - cap : from + j]; };
 #pragma unroll 4
-            for (int j = lane; j < need_i; j += per) {
-                const int at = from + j;
-                fresh[j] = p.ring[at >= cap ? at - cap : at];
-            }
+            for (int j = lane; j < need_i; j += per) row[old + j] = fresh(j);
             const int64_t to_i = static_cast<int64_t>(count) + s_to[i];
             for (int j = lane; j < gone_i && to_i + j < cap; j += per) {
                 const int at = static_cast<int>(to_i + j) - (cap - head);
                 p.ring[at < 0 ? at + cap : at] = row[j];
             }
+            if (with_slots) {
+                // rows past max_tokens belong to requests that were refused
+                const int64_t left = p.max_tokens - s_row[i];
+                const int rows = static_cast<int>(left < 0 ? 0 : (s_req[i] < left ? s_req[i] : left));
+                int64_t* dst = p.slots + s_row[i] * p.heads;
+                for (int e = lane; e < rows * p.heads; e += per) {
+                    const int t = e / p.heads;
+                    int64_t slot = -1;
+                    if (len_i >= 0) {
+                        const int64_t pos = static_cast<int64_t>(len_i) + t;
+                        const int pg = static_cast<int>(pos / kPage);
+                        slot = page_slot(p, pg < old ? row[pg] : fresh(pg - old), pos);
+                    }
+                    dst[e] = slot < 0 ? -1 : slot + (e - t * p.heads) * kPage;
+                }
+            }
         }
         __syncthreads();
+    }
+    if (with_slots) {                                    // input rows behind the last request's
+        for (int64_t e = rows_before * p.heads + tid; e < p.max_tokens * p.heads; e += NT) p.slots[e] = -1;
     }
     if (tid == 0) {
         const int taken = s_taken;
@@ -177,22 +178,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         p.state_out[0] = next >= cap ? next - cap : next;
         p.state_out[1] = count - taken + back;
     }
-    if (with_slots) {
-        for (int64_t t0 = 0; t0 < p.max_tokens; t0 += kPlanThreads) {
-            const int n = static_cast<int>(p.max_tokens - t0 < kPlanThreads ? p.max_tokens - t0 : kPlanThreads);
-            write_slots(p, t0, n, s_base);
-            __syncthreads();
-        }
-    }
 }
 
-// Slots of larger calls: one CTA per kSlotTile input rows, after plan_kernel.
+// Slots of larger calls, after plan_kernel: one CTA per kSlotTile input rows, one search per token for its request
+// (in shared memory up to kSlotBatch requests), then the tokens' H_kv slots with coalesced stores.
 __global__ void __launch_bounds__(kSlotTile) plan_slots_kernel(const PlanParams p) {
     __shared__ int64_t s_base[kSlotTile];
+    __shared__ int s_ends[kSlotBatch];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kSlotTile;
     const int n = static_cast<int>(p.max_tokens - t0 < kSlotTile ? p.max_tokens - t0 : kSlotTile);
-    write_slots(p, t0, n, s_base);
+    const int* ends = p.row_start + 1;
+    if (p.batch <= kSlotBatch) {
+        for (int i = tid; i < p.batch; i += kSlotTile) s_ends[i] = ends[i];
+        __syncthreads();
+        ends = s_ends;
+    }
+    int64_t base = -1;
+    if (tid < n) {
+        const int64_t token = t0 + tid;
+        int lo = 0, hi = p.batch;                        // the first request whose rows end after `token`
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (ends[mid] <= token) lo = mid + 1; else hi = mid;
+        }
+        if (lo < p.batch) {
+            const int start = p.start_pos[lo];
+            const int64_t pos = start + (token - (lo ? ends[lo - 1] : 0));
+            if (start >= 0) base = page_slot(p, p.table[static_cast<int64_t>(lo) * p.width + pos / kPage], pos);
+        }
+    }
+    s_base[tid] = base;
+    __syncthreads();
+    int64_t* dst = p.slots + t0 * p.heads;
+    for (int i = tid; i < n * p.heads; i += kSlotTile) {
+        const int t = i / p.heads, h = i - t * p.heads;
+        dst[i] = s_base[t] < 0 ? -1 : s_base[t] + h * kPage;
+    }
 }
 
 // ------------------------------------------------------------------------------- appending to pages
@@ -226,6 +249,10 @@ template <int W> struct Words;                           // W 32-bit words moved
 template <> struct Words<1> { using type = uint32_t; };
 template <> struct Words<2> { using type = uint2; };
 template <> struct Words<4> { using type = uint4; };
+template <int W> union Words32 {
+    typename Words<W>::type vec;
+    uint32_t w[W];
+};
 
 struct AppendParams {
     const void* k;                     // [n][H_kv][d] rows: token stride and head stride in elements
@@ -245,9 +272,9 @@ constexpr int kAppendWarps = 8;
 // One warp owns the page runs (consecutive input tokens of one kv head in one page) that start in its tile of
 // tokens, and follows the last one past the tile's end.  A run's rows are read once: stored to the pool and folded
 // into the page's channel bounds, which no other warp touches, so nothing is atomic and the result does not depend
-// on the order of warps.  A lane holds d / 32 channels of a row.
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendParams p) {
+// on the order of warps.  A lane holds d / 32 channels of a row.  VALUES: there is a value pool.
+template <typename T, int D, bool VALUES>
+__global__ void __launch_bounds__(32 * kAppendWarps, D == 256 && VALUES ? 2 : 3) append_kernel(const AppendParams p) {
     constexpr int W = D / 64;                            // words per lane and row
     constexpr int kBatch = 8;                            // rows in flight
     using Vec = typename Words<W>::type;
@@ -258,8 +285,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
     if (t0 >= p.n) return;
     const T* k = static_cast<const T*>(p.k) + h * p.k_head + lane * 2 * W;
     const T* v = static_cast<const T*>(p.v) + h * p.v_head + lane * 2 * W;
-    T* k_pool = static_cast<T*>(p.k_pool);
-    T* v_pool = static_cast<T*>(p.v_pool);
     auto slot_of = [&](int64_t t) -> int64_t {           // the slot of token t, -1 where the row is not stored
         const int64_t s = (t >= 0 && t < p.n) ? p.slots[t * p.heads + h] : -1;
         return s < p.rows ? s : -1;
@@ -276,34 +301,48 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
         int64_t token = t0 - 1 + at, ws = slot;          // the run's next token; slots of the window it lies in
         unsigned same = __ballot_sync(0xffffffffu, page == run) >> at;
         bool fresh = false;                              // the page's first token is new: its old bounds do not count
-        alignas(16) uint32_t lo[W], hi[W];
-        bool any = false;
+        bool first = true;
+        T* k_pool = static_cast<T*>(p.k_pool) + run * (kPage * D) + lane * 2 * W;
+        T* v_pool = static_cast<T*>(p.v_pool) + run * (kPage * D) + lane * 2 * W;
+        Words32<W> lo, hi, old_lo, old_hi;
         while (true) {
             const int len = ~same ? __ffs(~same) - 1 : 32;
             const unsigned mask = (len >= 32 ? 0xffffffffu : ((1u << len) - 1u)) << at;
-            fresh |= (__ballot_sync(0xffffffffu, ws % kPage == 0) & mask) != 0;
+            fresh |= (__ballot_sync(0xffffffffu, ws >= 0 && ws % kPage == 0) & mask) != 0;
             for (int j0 = 0; j0 < len; j0 += kBatch) {
-                Vec kr[kBatch], vr[kBatch];
+                Words32<W> kr[kBatch], vr[VALUES ? kBatch : 1];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     if (j0 + u < len) {
-                        kr[u] = *reinterpret_cast<const Vec*>(k + (token + j0 + u) * p.k_token);
-                        if (v_pool) vr[u] = *reinterpret_cast<const Vec*>(v + (token + j0 + u) * p.v_token);
+                        kr[u].vec = *reinterpret_cast<const Vec*>(k + (token + j0 + u) * p.k_token);
+                        if constexpr (VALUES) vr[u].vec = *reinterpret_cast<const Vec*>(v + (token + j0 + u) * p.v_token);
                     }
+                }
+                if (first) {                             // the old bounds come with the first rows
+                    if (p.bounds && !fresh) {
+                        const T* b = static_cast<const T*>(p.bounds) + run * 2 * D + lane * 2 * W;
+                        old_lo.vec = *reinterpret_cast<const Vec*>(b);
+                        old_hi.vec = *reinterpret_cast<const Vec*>(b + D);
+                    } else {
+                        old_lo = kr[0];
+                        old_hi = kr[0];
+                    }
+                    lo = kr[0];
+                    hi = kr[0];
+                    first = false;
                 }
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const int64_t s = __shfl_sync(0xffffffffu, ws, (at + j0 + u) & 31);
+                    // the run's rows lie in one page: a slot is the page's first plus 0 .. 15
+                    const int s = __shfl_sync(0xffffffffu, static_cast<int>(ws) & (kPage - 1), (at + j0 + u) & 31) * D;
                     if (j0 + u < len) {
-                        if (k_pool) *reinterpret_cast<Vec*>(k_pool + s * D + lane * 2 * W) = kr[u];
-                        if (v_pool) *reinterpret_cast<Vec*>(v_pool + s * D + lane * 2 * W) = vr[u];
-                        const uint32_t* w = reinterpret_cast<const uint32_t*>(&kr[u]);
+                        if (p.k_pool) *reinterpret_cast<Vec*>(k_pool + s) = kr[u].vec;
+                        if constexpr (VALUES) *reinterpret_cast<Vec*>(v_pool + s) = vr[u].vec;
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
-                            lo[i] = any ? min2<T>(lo[i], w[i]) : w[i];
-                            hi[i] = any ? max2<T>(hi[i], w[i]) : w[i];
+                            lo.w[i] = min2<T>(lo.w[i], kr[u].w[i]);
+                            hi.w[i] = max2<T>(hi.w[i], kr[u].w[i]);
                         }
-                        any = true;
                     }
                 }
             }
@@ -318,16 +357,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
         if (p.bounds) {
             T* b = static_cast<T*>(p.bounds) + run * 2 * D + lane * 2 * W;
             if (!fresh) {
-                const Vec ol = *reinterpret_cast<const Vec*>(b), oh = *reinterpret_cast<const Vec*>(b + D);
-                const uint32_t *pl = reinterpret_cast<const uint32_t*>(&ol), *ph = reinterpret_cast<const uint32_t*>(&oh);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    lo[i] = min2<T>(lo[i], pl[i]);
-                    hi[i] = max2<T>(hi[i], ph[i]);
+                    lo.w[i] = min2<T>(lo.w[i], old_lo.w[i]);
+                    hi.w[i] = max2<T>(hi.w[i], old_hi.w[i]);
                 }
             }
-            *reinterpret_cast<Vec*>(b) = *reinterpret_cast<Vec*>(lo);
-            *reinterpret_cast<Vec*>(b + D) = *reinterpret_cast<Vec*>(hi);
+            *reinterpret_cast<Vec*>(b) = lo.vec;
+            *reinterpret_cast<Vec*>(b + D) = hi.vec;
         }
     }
 }
@@ -343,109 +380,52 @@ struct SelectParams {
     int32_t* pages;                    // [B][H_kv][budget]
     int32_t* lens;                     // [B][H_kv]
     int heads, group, width, num_pages, budget, keep_first, keep_last;
-    int share_cap;                     // pages one CTA can hold
+    int room;                          // pages whose keys (and, unless SCORED, ids) select_kernel's shared memory holds
+    uint32_t* keys;                    // [B][H_kv][width]: keys of score_kernel (select_kernel's SCORED form)
 };
 
-constexpr int kSelThreads = 256;
-constexpr int kSelUnroll = 4;          // pages a lane group scores at a time
+constexpr int kScoreThreads = 256;     // threads that score pages together: a CTA of score_kernel, or of select_kernel
+constexpr int kScoreTile = 256;        // pages a CTA of score_kernel scores
+constexpr int kSortThreads = 1024;     // threads of select_kernel's SCORED form
 
-// shared memory of select_kernel: keys and page ids of the CTA's pages, then the query's positive and negative parts
-inline __host__ __device__ size_t select_smem(int share_cap, int group, int d) {
-    return static_cast<size_t>(share_cap) * 8 + static_cast<size_t>(group) * d * 8;
-}
+inline __host__ __device__ size_t query_smem(int group, int d) { return static_cast<size_t>(group) * d * 8; }
 
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t v;
-    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(v));
-    return v;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t v;
-    asm("mov.u32 %0, %%cluster_ctaid.x;" : "=r"(v));
-    return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A 32-bit word of the same shared-memory variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_load(const void* p, uint32_t rank) {
-    uint32_t a, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-
-// Scores and the `budget` best pages of one (sequence, kv head), by one cluster of CTAs that share its pages out in
-// order.
-//
-// The score of a page is max over the group's query heads of U_g = sum_c max(q_gc lo_c, q_gc hi_c), which is at least
-// q_g . k for every key in the page.  With lo <= hi the larger product is (q > 0 ? q hi : q lo), computed as two
-// fused multiply-adds of max(q, 0) with hi and min(q, 0) with lo: one of the products is a zero, and products of
-// 16-bit values are exact in fp32, so each step is a plain rounded addition.  The order of additions is part of the
-// operator (a lane's 8 channels as an even and an odd chain, then lanes i and i + half), so that the choice of pages
-// can be reproduced bit for bit.
-//
-// The choice itself is a radix selection over order-preserving keys, 8 bits a pass: every CTA counts its keys, the
-// cluster's counts are added up through distributed shared memory, and every CTA finds the same threshold.  Ties at
-// the threshold go to the lowest page index.
+// The query's heads of one kv head as max(q, 0) and min(q, 0) in shared memory, [G][2][d / 8][4]: lane l of a group
+// finds its channels 8 l .. 8 l + 7 in two 16-byte words without bank conflicts.
 template <typename T, int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-    constexpr int LP = D / 8;                            // lanes per page
-    constexpr int GW = 32 / LP;                          // lane groups per warp
-    constexpr int U = kSelUnroll;
-    static_assert(U == 4, "the reduction below spreads four pages over the lanes of a group");
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* qp = reinterpret_cast<float*>(smem);          // [G][2][LP][4]: max(q, 0)
-    float* qn = qp + p.group * D;                        // the same of min(q, 0)
-    uint32_t* keys = reinterpret_cast<uint32_t*>(qn + p.group * D);
-    int32_t* ids = reinterpret_cast<int32_t*>(keys + p.share_cap);
-    __shared__ uint32_t s_hist[4][256];
-    __shared__ uint32_t s_pick[2];
-    __shared__ uint32_t s_warp[kSelThreads / 32 + 1];
-    __shared__ uint32_t s_count[2];
-
-    const uint32_t cs = cluster_size(), rank = cluster_rank();
-    const int row = blockIdx.x / cs;
-    const int b = row / p.heads, h = row - b * p.heads;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t most = static_cast<int64_t>(p.width) * kPage;
-    int64_t len = p.seq_lens[b];
-    len = len < 0 ? 0 : (len > most ? most : len);
-    const int nb = static_cast<int>((len + kPage - 1) / kPage);
-    const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
-    int32_t* out = p.pages + static_cast<int64_t>(row) * p.budget;
-    if (rank == 0 && tid == 0)
-        p.lens[row] = static_cast<int>(nb <= p.budget ? len : len - static_cast<int64_t>(nb - p.budget) * kPage);
-    if (nb <= p.budget) {                                // every page is kept
-        for (int j = rank * kSelThreads + tid; j < p.budget; j += cs * kSelThreads) {
-            const int id = j < nb ? table[j] : -1;
-            out[j] = (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h;
-        }
-        return;
-    }
-    const int share = (nb + cs - 1) / cs;
-    const int p0 = rank * share;
-    const int cnt = nb - p0 < 0 ? 0 : (nb - p0 < share ? nb - p0 : share);
-    // ---- the query and the page ids
+__device__ __forceinline__ void load_query(const SelectParams& p, int b, int h, float* qp, float* qn) {
     const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<int64_t>(h) * p.group * D;
-    for (int i = tid; i < p.group * D; i += kSelThreads) {
+    for (int i = threadIdx.x; i < p.group * D; i += kScoreThreads) {
         const float x = static_cast<float>(q[i]);
         const int g = i / D, c = i % D;
         const int at = g * D + (c % 8 / 4) * (D / 2) + c / 8 * 4 + c % 4;
         qp[at] = fmaxf(x, 0.f);
         qn[at] = fminf(x, 0.f);
     }
-    for (int j = tid; j < cnt; j += kSelThreads) ids[j] = table[p0 + j];
-    for (int i = tid; i < 4 * 256; i += kSelThreads) s_hist[i / 256][i % 256] = 0;
-    __syncthreads();
-    // ---- scores
-    const int l = lane % LP;
-    const bool hi_half = (l & (LP / 2)) != 0, hi_quarter = (l & (LP / 4)) != 0;
+}
+
+// Keys (order-preserving bits of the scores) of pages p0 .. p0 + cnt - 1 of a row of nb pages, whose ids are in shared
+// memory, by the whole block.
+//
+// The score of a page is max over the group's query heads of U_g = sum_c max(q_gc lo_c, q_gc hi_c), which is at least
+// q_g . k for every key in the page.  With lo <= hi the larger product is (q > 0 ? q hi : q lo), computed as two
+// fused multiply-adds of max(q, 0) with hi and min(q, 0) with lo: one of the products is a zero, and products of
+// 16-bit values are exact in fp32, so each step is a plain rounded addition.  The order of additions is part of the
+// operator (a lane's 8 channels as an even and an odd chain, then lanes i and i + half), so that the choice of pages
+// can be reproduced bit for bit; it also rules out the tensor cores, whose order is not defined.
+template <typename T, int D, int U>
+__device__ __forceinline__ void score_pages(const SelectParams& p, int h, int nb, int p0, int cnt, const int32_t* ids,
+                                            const float* qp, const float* qn, uint32_t* keys) {
+    constexpr int LP = D / 8;                            // lanes per page
+    constexpr int GW = 32 / LP;                          // lane groups per warp
+    static_assert(U == 2 || U == 4, "the reduction below spreads two or four pages over the lanes of a group");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LP;
+    const bool upper = (l & (LP / 2)) != 0, odd = (l & (LP / 4)) != 0;
     const float4* qp4 = reinterpret_cast<const float4*>(qp) + l;
     const float4* qn4 = reinterpret_cast<const float4*>(qn) + l;
     const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + l * 8;
     const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
-    constexpr int kStep = (kSelThreads / 32) * GW * U;
+    constexpr int kStep = (kScoreThreads / 32) * GW * U;
     for (int base = (warp * GW + lane / LP) * U; base - (lane / LP) * U < cnt; base += kStep) {
         float2 lo[U][4], hi[U][4];
 #pragma unroll
@@ -481,19 +461,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 }
                 v[u] = acc.x + acc.y;
             }
-            // lanes i and i + LP/2 add up: the upper half goes on with pages 2, 3, the lower with 0, 1; then quarters
-            const float k0 = hi_half ? v[2] : v[0], k1 = hi_half ? v[3] : v[1];
-            const float g0 = hi_half ? v[0] : v[2], g1 = hi_half ? v[1] : v[3];
-            const float w0 = k0 + __shfl_xor_sync(0xffffffffu, g0, LP / 2);
-            const float w1 = k1 + __shfl_xor_sync(0xffffffffu, g1, LP / 2);
-            float s = (hi_quarter ? w1 : w0) + __shfl_xor_sync(0xffffffffu, hi_quarter ? w0 : w1, LP / 4);
+            // lanes i and i + LP/2 add up, the upper half going on with one half of the pages and the lower with the
+            // other; then quarters
+            float s;
+            if constexpr (U == 4) {
+                const float k0 = upper ? v[2] : v[0], k1 = upper ? v[3] : v[1];
+                const float g0 = upper ? v[0] : v[2], g1 = upper ? v[1] : v[3];
+                const float w0 = k0 + __shfl_xor_sync(0xffffffffu, g0, LP / 2);
+                const float w1 = k1 + __shfl_xor_sync(0xffffffffu, g1, LP / 2);
+                s = (odd ? w1 : w0) + __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, LP / 4);
+            } else {
+                s = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], LP / 2);
+                s += __shfl_xor_sync(0xffffffffu, s, LP / 4);
+            }
 #pragma unroll
             for (int o = LP / 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             // a NaN sum must not hide behind another head's number
             best = (s > best || s != s) ? s : best;
         }
-        const int j = base + (hi_half ? 2 : 0) + (hi_quarter ? 1 : 0);
-        if ((l & (LP / 4 - 1)) == 0 && j < cnt) {
+        const int j = base + (U == 4 ? (upper ? 2 : 0) + (odd ? 1 : 0) : (upper ? 1 : 0));
+        if ((l & (LP / U - 1)) == 0 && j < cnt) {
             const int at = p0 + j, id = ids[j];
             uint32_t bits = __float_as_uint(best + 0.f);             // -0 counts as 0
             bits = (bits >> 31) ? ~bits : bits | 0x80000000u;
@@ -502,78 +489,185 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             keys[j] = bits;
         }
     }
+}
+
+__device__ __forceinline__ int64_t select_len(const SelectParams& p, int b) {
+    const int64_t most = static_cast<int64_t>(p.width) * kPage, len = p.seq_lens[b];
+    return len < 0 ? 0 : (len > most ? most : len);
+}
+
+// Keys of a call with few rows, where a CTA per row would leave most of the GPU idle: a CTA per row and kScoreTile
+// pages.  Four pages per lane group share each read of the query from shared memory, which otherwise is the limit.
+template <typename T, int D>
+__global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* qp = reinterpret_cast<float*>(smem);
+    float* qn = qp + p.group * D;
+    __shared__ int32_t s_ids[kScoreTile];
+    static_assert(kScoreTile == kScoreThreads, "a thread per page id");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tiles = (p.width + kScoreTile - 1) / kScoreTile;
+    const int row = blockIdx.x / tiles, b = row / p.heads, h = row - b * p.heads;
+    const int64_t len = select_len(p, b);
+    const int p0 = (blockIdx.x - row * tiles) * kScoreTile;
+    load_query<T, D>(p, b, h, qp, qn);
+    if (p0 + threadIdx.x < p.width) s_ids[threadIdx.x] = p.table[static_cast<int64_t>(b) * p.width + p0 + threadIdx.x];
+    const int nb = static_cast<int>((len + kPage - 1) / kPage);
+    if (p0 >= nb || nb <= p.budget) return;
+    const int cnt = nb - p0 < kScoreTile ? nb - p0 : kScoreTile;
     __syncthreads();
-    // ---- the budget-th largest key of the cluster
-    uint32_t prefix = 0, mask = 0, need = static_cast<uint32_t>(p.budget);
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int j = tid; j < cnt; j += kSelThreads)
-            if ((keys[j] & mask) == prefix) atomicAdd(&s_hist[pass][(keys[j] >> shift) & 255u], 1u);
-        cluster_sync();
+    score_pages<T, D, 4>(p, h, nb, p0, cnt, s_ids, qp, qn, p.keys + static_cast<int64_t>(row) * p.width + p0);
+}
+
+// The `budget` best pages of one (sequence, kv head), by one CTA.  SCORED: score_kernel computes the keys, and this
+// grid is its programmatic dependent; else the CTA computes its row's keys first, several CTAs to an SM so that one
+// row's selection runs under another's loads.
+//
+// The choice is a radix selection: the keys' range is cut into 256 bins, the bin that holds the budget-th largest
+// key is found and cut again, until it goes in whole or holds one value, whose ties go to the lowest page index.  The
+// range starts at the smallest and largest score, not at the key's top bits, which all scores tend to share: two
+// passes usually do, and few keys fall into one bin at a time.  Pages kept in any case do not take part.
+template <typename T, int D, bool SCORED>
+__global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : 4) select_kernel(const SelectParams p) {
+    constexpr int NT = SCORED ? kSortThreads : kScoreThreads;
+    constexpr int NW = NT / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint32_t s_hist[2][256];
+    __shared__ uint32_t s_pick[3];
+    __shared__ uint32_t s_warp[NW], s_warp2[NW];
+    const int row = blockIdx.x;
+    const int b = row / p.heads, h = row - b * p.heads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
+    const int64_t len = select_len(p, b);
+    float* qp = reinterpret_cast<float*>(smem);
+    float* qn = qp + p.group * D;
+    uint32_t* room = reinterpret_cast<uint32_t*>(SCORED ? qp : qn + p.group * D);
+    int32_t* ids = reinterpret_cast<int32_t*>(room + p.room);
+    if constexpr (!SCORED) {                             // read while the length is on its way
+        load_query<T, D>(p, b, h, qp, qn);
+        for (int j = tid; j < p.width; j += NT) ids[j] = table[j];
+    }
+    if (tid < 256) s_hist[0][tid] = s_hist[1][tid] = 0;
+    const int nb = static_cast<int>((len + kPage - 1) / kPage);
+    int32_t* out = p.pages + static_cast<int64_t>(row) * p.budget;
+    if (tid == 0) p.lens[row] = static_cast<int>(nb <= p.budget ? len : len - static_cast<int64_t>(nb - p.budget) * kPage);
+    if (nb <= p.budget) {                                // every page is kept
+        for (int j = tid; j < p.budget; j += NT) {
+            const int id = j < nb ? table[j] : -1;
+            out[j] = (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h;
+        }
+        return;
+    }
+    const uint32_t* keys = room;
+    if constexpr (SCORED) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const uint32_t* src = p.keys + static_cast<int64_t>(row) * p.width;
+        if (nb <= p.room) {
+#pragma unroll 4
+            for (int j = tid; j < nb; j += NT) room[j] = __ldcg(src + j);
+        } else {
+            keys = src;                                  // a very long sequence: the passes read the L2 cache
+        }
+    } else {
+        __syncthreads();
+        score_pages<T, D, 2>(p, h, nb, 0, nb, ids, qp, qn, room);
+    }
+    __syncthreads();
+    // ---- the range of the keys that compete
+    const int c0 = p.keep_first, c1 = nb - p.keep_last;  // pages c0 .. c1 - 1
+    uint32_t least = 0xffffffffu, most = 0u;
+    for (int j = c0 + tid; j < c1; j += NT) {
+        least = min(least, keys[j]);
+        most = max(most, keys[j]);
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        s_warp[warp] = least;
+        s_warp2[warp] = most;
+    }
+    __syncthreads();
+    least = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0xffffffffu);
+    most = __reduce_max_sync(0xffffffffu, lane < NW ? s_warp2[lane] : 0u);
+    // ---- the threshold: keys above `least` + 2^bits - 1 are in, those below `least` out
+    uint32_t need = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);   // of the keys in between
+    int bits = 32 - __clz(static_cast<int>(most - least));
+    bool whole = need == 0;                              // nothing or everything in between is in
+    uint32_t bound = need == 0 ? 0xffffffffu : least;    // whole: keys from `bound` on are in
+    for (int pass = 0; !whole; ++pass) {
+        const int shift = bits > 8 ? bits - 8 : 0;
+        const uint32_t width = bits == 32 ? 0xffffffffu : (1u << bits) - 1u;
+        uint32_t* hist = s_hist[pass & 1];
+#pragma unroll 4
+        for (int j = c0 + tid; j < c1; j += NT) {
+            const uint32_t off = keys[j] - bound;
+            if (off <= width) atomicAdd(&hist[off >> shift], 1u);
+        }
+        __syncthreads();
         // thread t takes bin 255 - t, so that an inclusive scan counts the keys from the largest bin down
-        uint32_t c = 0;
-        for (uint32_t r = 0; r < cs; ++r) c += cluster_load(&s_hist[pass][255 - tid], r);
-        uint32_t incl = c;
+        uint32_t c = 0, incl = 0;
+        if (tid < 256) {
+            incl = c = hist[255 - tid];
+            s_hist[(pass & 1) ^ 1][tid] = 0;             // for the next pass
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        if (lane == 31) s_warp[warp] = incl;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += s_warp[w];
-        if (incl >= need && incl - c < need) {
-            s_pick[0] = 255u - tid;
-            s_pick[1] = incl - c;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            if (lane == 31) s_warp[warp] = incl;
         }
         __syncthreads();
-        prefix |= s_pick[0] << shift;
-        mask |= 255u << shift;
+        if (tid < 256) {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) incl += w < warp ? s_warp[w] : 0u;
+            if (incl >= need && incl - c < need) {       // one thread
+                s_pick[0] = 255u - tid;
+                s_pick[1] = incl - c;
+                s_pick[2] = incl;
+            }
+        }
+        __syncthreads();
+        bound += s_pick[0] << shift;
+        whole = s_pick[2] == need;
         need -= s_pick[1];
-        __syncthreads();
+        bits = shift;
+        if (shift == 0) break;
     }
-    // keys above `prefix` are in, and the first `need` of those equal to it
-    uint32_t mine = 0;                                   // above: low half, equal: high half
-    for (int j = tid; j < cnt; j += kSelThreads) mine += (keys[j] > prefix ? 1u : 0u) + (keys[j] == prefix ? 0x10000u : 0u);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_warp[warp] = mine;
+    // in: keys above `bound` (whole: from it on), the first `need` of those equal to it, and the pages kept in any case
+    const uint32_t from = whole ? bound : bound + 1;     // bound < 2^32 - 1: that key is of pages kept in any case
+    if (whole) need = 0;
+    const int chunk = ((nb + NW - 1) / NW + 31) & ~31;   // pages of a warp
+    const int j0 = warp * chunk, j1 = j0 + chunk < nb ? j0 + chunk : nb;
+    uint32_t n_in = 0, n_tie = 0;
+    for (int j = j0; j < j1; j += 32) {
+        const bool there = j + lane < j1;
+        const uint32_t key = there ? keys[j + lane] : 0u;
+        n_in += __popc(__ballot_sync(0xffffffffu, there && key >= from));
+        n_tie += __popc(__ballot_sync(0xffffffffu, there && key < from && key == bound));
+    }
+    __syncthreads();                                     // the sums before have been read
+    if (lane == 0) {
+        s_warp[warp] = n_in;
+        s_warp2[warp] = n_tie;
+    }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t a = 0;
-        for (int w = 0; w < kSelThreads / 32; ++w) a += s_warp[w];
-        s_count[0] = a & 0xffffu;
-        s_count[1] = a >> 16;
-    }
-    cluster_sync();
-    uint32_t above = 0, equal = 0;                       // in the CTAs before this one
-    for (uint32_t r = 0; r < rank; ++r) {
-        above += cluster_load(&s_count[0], r);
-        equal += cluster_load(&s_count[1], r);
-    }
-    for (int j0 = 0; j0 < cnt; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const uint32_t key = j < cnt ? keys[j] : 0u;
-        const bool gt = j < cnt && key > prefix, eq = j < cnt && key == prefix;
-        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) s_warp[warp] = __popc(mg) | (__popc(me) << 16);
-        __syncthreads();
-        uint32_t before = 0, all = 0;
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-            before += w < warp ? s_warp[w] : 0u;
-            all += s_warp[w];
+    uint32_t in_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+    uint32_t ties_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u);
+    const unsigned below = (1u << lane) - 1u;
+    for (int j = j0; j < j1; j += 32) {
+        const bool there = j + lane < j1;
+        const uint32_t key = there ? keys[j + lane] : 0u;
+        const bool in = there && key >= from, tie = there && key < from && key == bound;
+        const unsigned mi = __ballot_sync(0xffffffffu, in), mt = __ballot_sync(0xffffffffu, tie);
+        const uint32_t i_at = in_before + __popc(mi & below), t_at = ties_before + __popc(mt & below);
+        if (in || (tie && t_at < need)) {
+            const int id = SCORED ? table[j + lane] : ids[j + lane];
+            out[i_at + (t_at < need ? t_at : need)] = (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h;
         }
-        const uint32_t g_at = above + (before & 0xffffu) + __popc(mg & ((1u << lane) - 1u));
-        const uint32_t e_at = equal + (before >> 16) + __popc(me & ((1u << lane) - 1u));
-        if (gt || (eq && e_at < need)) {
-            const int id = ids[j];
-            out[g_at + (e_at < need ? e_at : need)] = (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h;
-        }
-        above += all & 0xffffu;
-        equal += all >> 16;
-        __syncthreads();
+        in_before += __popc(mi);
+        ties_before += __popc(mt);
     }
-    cluster_sync();                                      // a neighbour may still read this CTA's counts
 }
 
 // -------------------------------------------------------------------- attention over uncompressed pages
@@ -586,18 +680,21 @@ struct AttendPagesParams {
     const int32_t* lens;               // [units]
     float* out;                        // [B][H_q][d]
     float* partials;                   // [CTAs][2][16 + 8 d]
-    struct AttendPagesMeta* meta;      // [CTAs]
+    struct AttendPagesMeta* meta;      // [CTAs], or [rows] if the join goes by rows
     int64_t q_stride, k_page, v_page;  // elements; *_page: from one page to the next
     int units, mult;                   // table rows, and kv heads that share a table row (1 for selections)
     int width, num_ids, heads, group;
-    int min_pages;                     // pages a CTA takes at least
+    int min_share;                     // what a CTA takes at least
+    int rows_join;                     // rows (units * mult) if the join goes by rows, else 0
+    int join_heads;                    // heads that one CTA of the join takes
     float scale_log2;
 };
 
-// What the join needs of the CTA that starts inside a row: the row and its range on the flattened page axis.
+// What the join needs, of the row that a share starts in or, going by rows, of each row: the shares its pages lie in.
 struct AttendPagesMeta {
-    int64_t row_begin, row_end, share;
-    int row, pad;
+    int row;                           // -1: nothing to join
+    int first, last;
+    int pad;
 };
 
 template <int D>
@@ -605,12 +702,16 @@ struct PagesCfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kPageBytes = kPage * D * 2;                 // one page of keys (or values) of a kv head
-    static constexpr int kStages = (D == 64) ? 6 : 3;                // pages of keys and values in flight per warp
-    static constexpr int kCtasPerSm = (D == 256) ? 1 : 2;
+    static constexpr int kStages = (D == 64) ? 4 : 3;                // pages of keys and values in flight per warp
+    static constexpr int kCtasPerSm = (D == 64) ? 3 : (D == 128) ? 2 : 1;
     static constexpr int kRing = kWarps * kStages * 2 * kPageBytes;
+    // what a row costs besides its pages (its query, the joining of the warps' parts), in pages; a multiple of kWarps
+    static constexpr int kRowCost = D == 64 ? 8 : 4;
     static constexpr int kHeadStride = D + 4;                        // spreads the accumulator rows over the banks
-    static constexpr int kComb = 16 + 8 * kHeadStride;               // floats per warp: m[8], l[8], O[8][D + 4]
-    static constexpr int kSmem = kRing + kWarps * kComb * 4;
+    // floats per warp: m[8], l[8], O[G][D + 4].  What a group of fewer than 8 heads leaves free lets the join's CTAs
+    // become resident before the last share is done.
+    static constexpr __host__ __device__ int comb(int group) { return 16 + group * kHeadStride; }
+    static constexpr int smem(int group) { return kRing + kWarps * comb(group) * 4; }
     static constexpr int kPart = 16 + 8 * D;                         // floats per partial: m[8], l[8], O[8][D]
 };
 
@@ -676,25 +777,28 @@ template <> struct Weights<__nv_bfloat16> {
     }
 };
 
-// A place on the flattened page axis: units in order, the kv heads of a unit in order, then pages.
+// A place on the flattened axis: units in order, the kv heads of a unit in order, and for each of these rows
+// kRowCost places for the row itself, then its pages.  Units without a page take no place.  The host refuses tables
+// whose axis could reach 2^31.
 struct PageCursor {
+    int x;                             // of page pg of row (unit, m)
     int unit, m, pg, pages;            // pages: of this unit
 };
 
-__device__ __forceinline__ int64_t unit_len(const AttendPagesParams& p, int u) {
-    const int64_t most = static_cast<int64_t>(p.width) * kPage;
-    const int64_t t = p.lens[u];
+__device__ __forceinline__ int unit_len(const AttendPagesParams& p, int u) {
+    const int t = p.lens[u], most = p.width * kPage;     // width < 2^27
     return t < 0 ? 0 : (t > most ? most : t);
 }
-__device__ __forceinline__ int unit_pages(const AttendPagesParams& p, int u) {
-    return static_cast<int>((unit_len(p, u) + kPage - 1) / kPage);
-}
+__device__ __forceinline__ int unit_pages(const AttendPagesParams& p, int u) { return (unit_len(p, u) + kPage - 1) / kPage; }
 
 // Moves on by n pages; past the last page the cursor stays behind the last unit.
+template <int ROW_COST>
 __device__ __forceinline__ void advance(const AttendPagesParams& p, PageCursor& c, int n) {
     c.pg += n;
+    c.x += n;
     while (c.pg >= c.pages) {
         c.pg -= c.pages;
+        c.x += ROW_COST;
         if (++c.m == p.mult) {
             c.m = 0;
             do {
@@ -707,10 +811,10 @@ __device__ __forceinline__ void advance(const AttendPagesParams& p, PageCursor& 
 
 // Attention of one new token over a paged cache.  softmax(scale q k^T) v needs every key and value once and a few
 // operations per byte, so the kernel is bound by how fast pages can be read, and the grid is laid out for that alone:
-// all pages of the call, in the order (table row, kv head, page), are cut into equal shares, one per resident CTA,
-// whatever the lengths of the sequences are.  A share covers parts of one or several rows (a row: one sequence and
-// kv head with its query heads); a row that lies inside one share is finished there, and attend_pages_join_kernel
-// joins the others.  The running maximum and sum (fp32) make the split exact up to rounding.
+// all pages of the call, in the order (table row, kv head, page), are cut into shares of equal cost, one per resident
+// CTA, whatever the lengths of the sequences are.  A share covers parts of one or several rows (a row: one sequence
+// and kv head with its query heads, whose own cost counts as kRowCost pages); a row that lies inside one share is
+// finished there, and attend_pages_join_kernel joins the others.  The running maximum and sum (fp32) make the split exact up to rounding.
 //
 // Warp w of a CTA takes pages w, w + 4, ... of the share and keeps kStages of them in flight in its own ring of
 // shared memory with 16-byte cp.async copies, so no warp waits for another until a row ends.  16-byte chunk c of a
@@ -729,78 +833,84 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
     constexpr float kSlack = 3.f;                        // a logit may pass the running maximum by this before it moves
     extern __shared__ __align__(16) uint8_t smem[];
     float* comb = reinterpret_cast<float*>(smem + C::kRing);
-    int64_t* s_setup = reinterpret_cast<int64_t*>(comb); // used before the first row ends only
+    int* s_setup = reinterpret_cast<int*>(comb);         // used before the first row ends only
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gid = lane >> 2, tig = lane & 3;
     const int G = p.group;
 
-    // ---- this CTA's share
-    int64_t sum = 0;
-    for (int u = tid; u < p.units; u += C::kThreads) sum += unit_pages(p, u);
+    // ---- this CTA's share.  Thread t looks at units t * per .. t * per + per - 1.
+    auto unit_cost = [&](int u) -> int {                 // of each of the unit's rows
+        const int n = unit_pages(p, u);
+        return n ? n + C::kRowCost : 0;
+    };
+    const int per = (p.units + C::kThreads - 1) / C::kThreads;
+    const int u0 = tid * per, u1 = u0 + per < p.units ? u0 + per : p.units;
+    int own = 0;
+#pragma unroll 4
+    for (int u = u0; u < u1; ++u) own += unit_cost(u);
+    int incl = own;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_setup[warp] = sum;
-    // rows without a token are nobody's page: their zeros are written here
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
-        if (unit_pages(p, u) == 0) {
-            float* o = p.out + static_cast<int64_t>(u) * p.mult * G * D;
-            for (int i = tid; i < p.mult * G * D; i += C::kThreads) o[i] = 0.f;
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
     }
+    if (lane == 31) s_setup[warp] = incl;
     __syncthreads();
-    const int64_t total = (s_setup[0] + s_setup[1] + s_setup[2] + s_setup[3]) * p.mult;
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < p.min_pages) share = p.min_pages;
-    const int64_t x0 = blockIdx.x * share;
-    const int64_t x1 = x0 + share < total ? x0 + share : total;
-    if (x0 >= total) {
-        if (tid == 0) p.meta[blockIdx.x].row = -1;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+        if (w < warp) incl += s_setup[w];
+        total += s_setup[w];
+    }
+    total *= p.mult;
+    int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    if (share < p.min_share) share = p.min_share;
+    // past the last share x0 may pass 2^31: unsigned
+    const unsigned start = blockIdx.x * static_cast<unsigned>(share);
+    auto write_zeros = [&]() {                           // rows without a token are nobody's page
+        for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+            if (unit_pages(p, u) == 0) {
+                float* o = p.out + static_cast<int64_t>(u) * p.mult * G * D;
+                for (int i = tid; i < p.mult * G * D; i += C::kThreads) o[i] = 0.f;
+                if (p.rows_join)
+                    for (int i = tid; i < p.mult; i += C::kThreads) p.meta[u * p.mult + i].row = -1;
+            }
+        }
+    };
+    if (start >= static_cast<unsigned>(total)) {
+        if (!p.rows_join && tid == 0) p.meta[blockIdx.x].row = -1;
+        write_zeros();
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
     }
-    int64_t carry = 0;                                   // pages of the units before this tile of units
-    for (int u0 = 0; u0 < p.units; u0 += C::kThreads) {
-        const int n = u0 + tid < p.units ? unit_pages(p, u0 + tid) : 0;
-        int64_t incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
+    const int x0 = static_cast<int>(start), x1 = total - x0 < share ? total : x0 + share;
+    {
+        int begin = (incl - own) * p.mult;
+        if (x0 >= begin && x0 < incl * p.mult) {         // one thread: its units are read again
+            for (int u = u0; u < u1; ++u) {
+                const int cost = unit_cost(u), end = begin + cost * p.mult;
+                if (x0 < end) {
+                    s_setup[C::kWarps] = u;
+                    s_setup[C::kWarps + 1] = x0 - begin;
+                    s_setup[C::kWarps + 2] = cost;
+                    break;
+                }
+                begin = end;
+            }
         }
-        __syncthreads();                                 // the sums above, and the tile before, have been read
-        if (lane == 31) s_setup[warp] = incl;
-        __syncthreads();
-        int64_t all = 0;
-#pragma unroll
-        for (int w = 0; w < C::kWarps; ++w) {
-            if (w < warp) incl += s_setup[w];
-            all += s_setup[w];
-        }
-        const int64_t begin = (carry + incl - n) * p.mult, end = (carry + incl) * p.mult;
-        if (x0 >= begin && x0 < end) {
-            s_setup[4] = u0 + tid;
-            s_setup[5] = x0 - begin;
-            s_setup[6] = n;
-        }
-        carry += all;
-        if (carry * p.mult > x0) break;
     }
     __syncthreads();
-    PageCursor seg;
-    seg.unit = static_cast<int>(s_setup[4]);
-    seg.pages = static_cast<int>(s_setup[6]);
-    seg.m = static_cast<int>(s_setup[5] / seg.pages);
-    seg.pg = static_cast<int>(s_setup[5] % seg.pages);
-    __syncthreads();                                     // the rows' results may overwrite the set-up words
-    if (tid == 0) {
-        AttendPagesMeta m;
-        m.row_begin = x0 - seg.pg;
-        m.row_end = m.row_begin + seg.pages;
-        m.share = share;
-        m.row = seg.unit * p.mult + seg.m;
-        m.pad = 0;
-        p.meta[blockIdx.x] = m;
+    PageCursor seg;                                      // the first page at or behind x0
+    {
+        const int off = s_setup[C::kWarps + 1], cost = s_setup[C::kWarps + 2];
+        seg.unit = s_setup[C::kWarps];
+        seg.pages = cost - C::kRowCost;
+        seg.m = off / cost;
+        const int in_row = off - seg.m * cost;
+        seg.pg = in_row < C::kRowCost ? 0 : in_row - C::kRowCost;
+        seg.x = x0 - in_row + C::kRowCost + seg.pg;
     }
+    __syncthreads();                                     // the rows' results may overwrite the set-up words
 
     // ---- the copy ring
     const T* k_pool = static_cast<const T*>(p.k_pool);
@@ -808,11 +918,12 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
     const uint32_t ring = smem_u32(smem) + warp * S * 2 * C::kPageBytes;
     constexpr int CR = D / 8;                            // chunks per row
     constexpr int kCopies = kPage * CR / 32;             // 16-byte copies per lane, page and tensor
-    PageCursor ld = seg;
-    int64_t xl = x0 + warp;                              // the next page to be copied
-    if (warp) advance(p, ld, warp);
+    // warp w takes the pages whose place is w modulo kWarps
+    auto first_of = [&](int x) { return (warp - x) & (C::kWarps - 1); };
+    PageCursor ld = seg;                                 // the next page to be copied
+    if (first_of(seg.x)) advance<C::kRowCost>(p, ld, first_of(seg.x));
     auto page_id = [&]() -> int {
-        return xl < x1 ? __ldg(p.table + static_cast<int64_t>(ld.unit) * p.width + ld.pg) : -1;
+        return ld.x < x1 ? __ldg(p.table + static_cast<int64_t>(ld.unit) * p.width + ld.pg) : -1;
     };
     unsigned good = 0;                                   // bit s: stage s holds a page (its id named one)
     auto issue = [&](int s, int id, int m) {
@@ -844,30 +955,38 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         for (int s = 0; s < S; ++s) {
             id[s] = page_id();
             m[s] = ld.m;
-            xl += C::kWarps;
-            if (xl < x1) advance(p, ld, C::kWarps);
+            if (ld.x < x1) advance<C::kRowCost>(p, ld, C::kWarps);
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) issue(s, id[s], m[s]);
         next_id = page_id();
         next_m = ld.m;
     }
+    // while the first pages are on their way
+    write_zeros();
+    if (!p.rows_join && tid == 0) {
+        // the row that crosses into this share, if this is its first crossing
+        const int row_begin = seg.x - seg.pg, first = row_begin / share;
+        AttendPagesMeta m;
+        m.row = row_begin < x0 && first == static_cast<int>(blockIdx.x) - 1 ? seg.unit * p.mult + seg.m : -1;
+        m.first = first;
+        m.last = (row_begin + seg.pages - 1) / share;
+        m.pad = 0;
+        p.meta[blockIdx.x] = m;
+    }
 
     // ---- rows
     int stage = 0;
-    int64_t xw = x0 + warp;                              // this warp's next page
-    int64_t xs = x0;
     const int mrow = (lane & 7) + ((lane >> 4) << 3);    // ldmatrix: matrices 0, 1 are rows 0-7, matrices 2, 3 rows 8-15
     const int mchunk = ((lane >> 3) & 1) ^ (lane & 7);   // and matrices 1, 3 the odd 16-byte chunk
-    while (xs < x1) {
-        const int64_t len = unit_len(p, seg.unit);
-        const int64_t xe = xs + (seg.pages - seg.pg) < x1 ? xs + (seg.pages - seg.pg) : x1;
-        const int64_t row = static_cast<int64_t>(seg.unit) * p.mult + seg.m;
-        const int64_t row_begin = xs - seg.pg, row_end = row_begin + seg.pages;
+    while (seg.x < x1) {
+        const int len = unit_len(p, seg.unit);
+        const int row = seg.unit * p.mult + seg.m;
+        const int row_begin = seg.x - seg.pg, row_end = row_begin + seg.pages;
+        const int xe = row_end < x1 ? row_end : x1;
         uint32_t qa[KS][2];
         {
-            const int64_t b = row / p.heads;
-            const int h = static_cast<int>(row - b * p.heads);
+            const int b = row / p.heads, h = row - b * p.heads;
             const T* q = static_cast<const T*>(p.q) + b * p.q_stride + (static_cast<int64_t>(h) * G + gid) * D + 2 * tig;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -879,11 +998,11 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
 #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m_run = -INFINITY, m_thr = -INFINITY, m_off = 0.f, l_run = 0.f;
-        for (; xw < xe; xw += C::kWarps) {
+        for (int x = seg.x + first_of(seg.x); x < xe; x += C::kWarps) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
             __syncwarp();
-            const int64_t left = len - (xw - row_begin) * kPage;
-            const int valid = left < kPage ? static_cast<int>(left) : kPage;
+            const int left = len - (x - row_begin) * kPage;
+            const int valid = left < kPage ? left : kPage;
             if (good >> stage & 1u) {
                 const uint32_t kb = ring + stage * 2 * C::kPageBytes + mrow * (2 * D);
                 float sc[2][2][4] = {};
@@ -948,8 +1067,7 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
             }
             __syncwarp();                                        // every lane is done with the stage
             issue(stage, next_id, next_m);
-            xl += C::kWarps;
-            if (xl < x1) advance(p, ld, C::kWarps);
+            if (ld.x < x1) advance<C::kRowCost>(p, ld, C::kWarps);
             next_id = page_id();
             next_m = ld.m;
             stage = stage + 1 == S ? 0 : stage + 1;
@@ -957,7 +1075,8 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         // ---- the warps' parts of this row
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-        float* mine = comb + warp * C::kComb;
+        const int kComb = C::comb(G);
+        float* mine = comb + warp * kComb;
         if (tig == 0) {
             mine[gid] = m_run;
             mine[8 + gid] = l_run;
@@ -966,27 +1085,36 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         for (int i = 0; i < KS; ++i) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                mine[16 + (2 * tig + (e & 1)) * C::kHeadStride + 16 * i + gid + 8 * (e >> 1)] = o[i][e];
+                if (2 * tig + (e & 1) < G)
+                    mine[16 + (2 * tig + (e & 1)) * C::kHeadStride + 16 * i + gid + 8 * (e >> 1)] = o[i][e];
         }
         __syncthreads();
         const bool whole = row_begin >= x0 && row_end <= x1;
         // a share has at most two rows that it does not finish: one that began before it, one that goes on behind it
-        float* part = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (xs == x0 ? 0 : 1)) * C::kPart;
+        float* part = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (row_begin < x0 ? 0 : 1)) * C::kPart;
+        if (p.rows_join && tid == 0 && row_begin >= x0) {        // the row begins here
+            AttendPagesMeta m;
+            m.row = whole ? -1 : row;
+            m.first = blockIdx.x;
+            m.last = (row_end - 1) / share;
+            m.pad = 0;
+            p.meta[row] = m;
+        }
         for (int i = tid; i < G * D; i += C::kThreads) {
             const int g = i / D, col = i % D;
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, comb[w * C::kComb + g]);
+            for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, comb[w * kComb + g]);
             const float Mu = M == -INFINITY ? 0.f : M;
             float L = 0.f, O = 0.f;
 #pragma unroll
             for (int w = 0; w < C::kWarps; ++w) {
-                const float f = exp2_approx(comb[w * C::kComb + g] - Mu);
-                L = fmaf(comb[w * C::kComb + 8 + g], f, L);
-                O = fmaf(comb[w * C::kComb + 16 + g * C::kHeadStride + col], f, O);
+                const float f = exp2_approx(comb[w * kComb + g] - Mu);
+                L = fmaf(comb[w * kComb + 8 + g], f, L);
+                O = fmaf(comb[w * kComb + 16 + g * C::kHeadStride + col], f, O);
             }
             if (whole) {
-                p.out[(row * G + g) * D + col] = L > 0.f ? O / L : 0.f;
+                p.out[(static_cast<int64_t>(row) * G + g) * D + col] = L > 0.f ? O / L : 0.f;
             } else {
                 part[16 + g * D + col] = O;
                 if (col == 0) {
@@ -996,78 +1124,86 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
             }
         }
         __syncthreads();                                         // the next row's parts go to the same place
-        advance(p, seg, seg.pages - seg.pg);
-        xs = xe;
+        advance<C::kRowCost>(p, seg, seg.pages - seg.pg);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the rows that lie in several shares: CTA (i, g) takes head g of the row that crosses from share i - 1 into
-// share i, if that is the row's first crossing.  out = sum O 2^(m - M) / sum l 2^(m - M).
-constexpr int kJoinThreads = 512;
+// Joins the rows that lie in several shares.  out = sum O 2^(m - M) / sum l 2^(m - M).  With no more rows than shares
+// CTA x takes row x, else the row that crosses from share x into share x + 1 if that is the row's first crossing; CTA y
+// takes heads y * join_heads ... A thread has four columns of a head; slices of the block take every so-manieth part
+// and are added up at the end.
+constexpr int kJoinThreads = 256;      // at most
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_pages_join_kernel(const AttendPagesParams p) {
+__global__ void __launch_bounds__(kJoinThreads, 4) attend_pages_join_kernel(const AttendPagesParams p) {
     constexpr int kPart = PagesCfg<D>::kPart;
-    constexpr int kSlices = kJoinThreads / D;
     constexpr int kBatch = 8;                            // parts a thread reads at a time
-    __shared__ float s_o[kSlices][D];
-    __shared__ float s_ml[kSlices][2];
+    __shared__ float4 s_o[kJoinThreads];
+    __shared__ float2 s_ml[kJoinThreads];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t i = blockIdx.x + 1;
-    const int g = blockIdx.y, tid = threadIdx.x, col = tid % D, slice = tid / D;
-    const AttendPagesMeta m = p.meta[i];
-    if (m.row < 0 || m.row_begin >= i * m.share || m.row_begin < (i - 1) * m.share) return;
-    const int first = static_cast<int>(i - 1), last = static_cast<int>((m.row_end - 1) / m.share);
-    // the row is the first share's second part unless that share begins with it
-    const int slot = m.row_begin == (i - 1) * m.share ? 0 : 1;
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int k0 = first + slice; k0 <= last; k0 += kSlices * kBatch) {
-        float mv[kBatch], lv[kBatch], ov[kBatch];
+    const AttendPagesMeta m = p.meta[p.rows_join ? blockIdx.x : blockIdx.x + 1];
+    if (m.row < 0) return;
+    const int g0 = blockIdx.y * p.join_heads;
+    const int heads = p.group - g0 < p.join_heads ? p.group - g0 : p.join_heads;
+    const int items = heads * (D / 4), slices = blockDim.x / items;
+    const int tid = threadIdx.x, slice = tid / items, item = tid - slice * items;
+    const int g = g0 + item / (D / 4), c = item % (D / 4) * 4;
+    const int first = m.first, last = m.last;
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = slice < slices ? first + slice : last + 1; k0 <= last; k0 += slices * kBatch) {
+        float mv[kBatch], lv[kBatch];
+        float4 ov[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int k = k0 + u * kSlices;
-            const float* ps = p.partials + (static_cast<int64_t>(k <= last ? k : first) * 2 +
-                                            ((k == first || k > last) ? slot : 0)) * kPart;
-            mv[u] = k <= last ? __ldcg(ps + g) : -INFINITY;
+            // the row is the second unfinished one of the share it begins in, and the first of the others
+            const int k = k0 + u * slices <= last ? k0 + u * slices : k0;
+            const float* ps = p.partials + (static_cast<int64_t>(k) * 2 + (k == first ? 1 : 0)) * kPart;
+            mv[u] = k0 + u * slices <= last ? __ldcg(ps + g) : -INFINITY;
             lv[u] = __ldcg(ps + 8 + g);
-            ov[u] = __ldcg(ps + 16 + g * D + col);
+            ov[u] = __ldcg(reinterpret_cast<const float4*>(ps + 16 + g * D + c));
         }
         float Mn = M;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) Mn = fmaxf(Mn, mv[u]);
         const float Mu = Mn == -INFINITY ? 0.f : Mn;
-        const float c = exp2_approx(M - Mu);
-        L *= c;
-        O *= c;
+        float f = exp2_approx(M - Mu);
+        L *= f;
+        O.x *= f; O.y *= f; O.z *= f; O.w *= f;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const float f = exp2_approx(mv[u] - Mu);
+            f = exp2_approx(mv[u] - Mu);                 // 0 for what is read twice
             L = fmaf(lv[u], f, L);
-            O = fmaf(ov[u], f, O);
+            O.x = fmaf(ov[u].x, f, O.x);
+            O.y = fmaf(ov[u].y, f, O.y);
+            O.z = fmaf(ov[u].z, f, O.z);
+            O.w = fmaf(ov[u].w, f, O.w);
         }
         M = Mn;
     }
-    s_o[slice][col] = O;
-    if (col == 0) {
-        s_ml[slice][0] = M;
-        s_ml[slice][1] = L;
-    }
+    s_o[tid] = O;
+    s_ml[tid] = make_float2(M, L);
     __syncthreads();
     if (slice == 0) {
-        float Mt = s_ml[0][0];
-#pragma unroll
-        for (int k = 1; k < kSlices; ++k) Mt = fmaxf(Mt, s_ml[k][0]);
-        const float Mu = Mt == -INFINITY ? 0.f : Mt;
-        float Lt = 0.f, Ot = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSlices; ++k) {
-            const float f = exp2_approx(s_ml[k][0] - Mu);
-            Lt = fmaf(s_ml[k][1], f, Lt);
-            Ot = fmaf(s_o[k][col], f, Ot);
+        for (int k = 1; k < slices; ++k) M = fmaxf(M, s_ml[k * items + item].x);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < slices; ++k) {
+            const float2 ml = s_ml[k * items + item];
+            const float4 o = s_o[k * items + item];
+            const float f = exp2_approx(ml.x - Mu);
+            L = fmaf(ml.y, f, L);
+            O.x = fmaf(o.x, f, O.x);
+            O.y = fmaf(o.y, f, O.y);
+            O.z = fmaf(o.z, f, O.z);
+            O.w = fmaf(o.w, f, O.w);
         }
-        p.out[(static_cast<int64_t>(m.row) * p.group + g) * D + col] = Lt > 0.f ? Ot / Lt : 0.f;
+        const float r = L > 0.f ? 1.f / L : 0.f;
+        O.x *= r; O.y *= r; O.z *= r; O.w *= r;
+        *reinterpret_cast<float4*>(p.out + (static_cast<int64_t>(m.row) * p.group + g) * D + c) = O;
     }
 }
 

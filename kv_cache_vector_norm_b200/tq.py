@@ -79,7 +79,7 @@ class SelectArgs(ctypes.Structure):
         ("num_pages", ctypes.c_int), ("budget", ctypes.c_int), ("keep_first", ctypes.c_int),
         ("keep_last", ctypes.c_int), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("bounds", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("pages", ctypes.c_void_p),
-        ("lens", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -143,6 +143,7 @@ SIGNATURES = {
                                        ctypes.c_void_p, ctypes.c_void_p]),
     "tq_plan_pages": (ctypes.c_int, [ctypes.POINTER(PlanArgs), ctypes.c_void_p]),
     "tq_append_pages": (ctypes.c_int, [ctypes.POINTER(AppendArgs), ctypes.c_void_p]),
+    "tq_select_pages_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(SelectArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "tq_select_pages": (ctypes.c_int, [ctypes.POINTER(SelectArgs), ctypes.c_void_p]),
     "tq_attend_pages_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(AttendPagesArgs),
                                                        ctypes.POINTER(ctypes.c_size_t)]),
@@ -542,6 +543,10 @@ def attend_decode_noalloc(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv
 PAGE = 16                                               # tokens per page
 _PAGE_DTYPES = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
 
+# The raw handle of a device's current stream, without building a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _page_dtype(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -552,22 +557,29 @@ def _page_dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _need(t: torch.Tensor, name: str, dtype, shape, device):
-    """Pointer of a contiguous tensor of this dtype, shape (None: any extent) and device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
-    if t.dim() != len(shape) or any(w is not None and w != s for s, w in zip(t.shape, shape)) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {list(shape)} (None: any), got {list(t.shape)}")
-    return t.data_ptr()
+def _need(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> int:
+    """Address of a contiguous tensor of this dtype, shape and device.  A decode step's calls take a few microseconds on
+    the GPU and pass up to ten tensors, so the checks are one expression."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
+    if t.dtype is not dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
+    raise ValueError(f"{name} must be contiguous with shape {list(shape)}, got {list(t.shape)}")
 
 
-def _run_on(device: torch.device, name: str, args):
-    """Enqueue a call on the current stream of `device`, whichever device is current."""
-    if device.index == torch.cuda.current_device():
-        _check(name, getattr(LIB, name)(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream))
+def _run_on(device: torch.device, name: str, fn, args, second=None):
+    """Make a call with `device` current; `second` is its second argument, by default that device's current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(args, _raw_stream(index) if second is None else second)
     else:
         with torch.cuda.device(device):
-            _check(name, getattr(LIB, name)(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream))
+            status = fn(args, _raw_stream(index) if second is None else second)
+    if status != TQ_OK:
+        raise TQError(name, status)
 
 
 @dataclass
@@ -606,23 +618,25 @@ def plan_pages(new_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torc
         seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
     if free_state_out is None:
         free_state_out = torch.empty(2, dtype=torch.int32, device=dev)
-    i32 = torch.int32
-    a = PlanArgs(b, num_kv_heads, block_table.shape[-1], free_pages.shape[0], max_tokens,
+    i32, width, num_pages = torch.int32, block_table.shape[-1], free_pages.shape[0]
+    a = PlanArgs(b, num_kv_heads, width, num_pages, max_tokens,
                  _need(new_lens, "new_lens", i32, (b,), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
-                 _need(block_table, "block_table", i32, (b, None), dev),
-                 _need(free_pages, "free_pages", i32, (None,), dev), _need(free_state, "free_state", i32, (2,), dev),
+                 _need(block_table, "block_table", i32, (b, width), dev),
+                 _need(free_pages, "free_pages", i32, (num_pages,), dev), _need(free_state, "free_state", i32, (2,), dev),
                  _need(slots, "slots", torch.int64, (max_tokens * num_kv_heads,), dev),
                  _need(row_start, "row_start", i32, (b + 1,), dev), _need(start_pos, "start_pos", i32, (b,), dev),
                  _need(seq_lens_out, "seq_lens_out", i32, (b,), dev),
                  _need(free_state_out, "free_state_out", i32, (2,), dev))
-    _run_on(dev, "tq_plan_pages", a)
+    _run_on(dev, "tq_plan_pages", LIB.tq_plan_pages, a)
     return PagePlan(slots, row_start, start_pos, seq_lens_out, free_state_out)
 
 
-def _rows(t: torch.Tensor, name: str, like: torch.Tensor):
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or t.stride(2) != 1:
+def _rows(t: torch.Tensor, name: str, k: torch.Tensor, device):
+    """Address and strides of k, or of v beside it."""
+    token, head, unit = t.stride()
+    if unit != 1 or (t is not k and (t.shape != k.shape or t.dtype is not k.dtype or t.device != device)):
         raise ValueError(f"{name} must be [N, H_kv, d] like k, with unit stride along d")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), token, head
 
 
 def append_pages(k: torch.Tensor, v: torch.Tensor | None, slots: torch.Tensor, *, k_pool: torch.Tensor | None = None,
@@ -635,33 +649,36 @@ def append_pages(k: torch.Tensor, v: torch.Tensor | None, slots: torch.Tensor, *
         raise ValueError("k must be [N, H_kv, d]")
     n, h, d = k.shape
     dev = k.device
-    pages = next((t.shape[0] for t in (k_pool, v_pool, bounds) if t is not None), 0)
+    some = k_pool if k_pool is not None else v_pool if v_pool is not None else bounds
+    pages = some.shape[0] if some is not None else 0
     if v_pool is not None and v is None:
         raise ValueError("v_pool needs v")
-    kp, k_tok, k_head = _rows(k, "k", k)
-    vp, v_tok, v_head = _rows(v, "v", k) if v is not None else (None, 0, 0)
+    kp, k_tok, k_head = _rows(k, "k", k, dev)
+    vp, v_tok, v_head = _rows(v, "v", k, dev) if v is not None else (None, 0, 0)
+    kt, shape = k.dtype, (pages, h, PAGE, d)
     a = AppendArgs(dtype, d, h, pages, n, kp, vp, k_tok, k_head, v_tok, v_head,
                    _need(slots, "slots", torch.int64, (n * h,), dev),
-                   _need(k_pool, "k_pool", k.dtype, (pages, h, PAGE, d), dev) if k_pool is not None else None,
-                   _need(v_pool, "v_pool", k.dtype, (pages, h, PAGE, d), dev) if v_pool is not None else None,
-                   _need(bounds, "bounds", k.dtype, (pages, h, 2, d), dev) if bounds is not None else None)
-    _run_on(dev, "tq_append_pages", a)
+                   _need(k_pool, "k_pool", kt, shape, dev) if k_pool is not None else None,
+                   _need(v_pool, "v_pool", kt, shape, dev) if v_pool is not None else None,
+                   _need(bounds, "bounds", kt, (pages, h, 2, d), dev) if bounds is not None else None)
+    _run_on(dev, "tq_append_pages", LIB.tq_append_pages, a)
 
 
 def _q_rows(q: torch.Tensor):
     """dtype code, sizes and batch stride of a query [B, H_q, d] whose sequences may lie apart."""
-    dtype = _page_dtype(q, "q")
-    if q.dim() != 3 or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
+    dtype, shape, strides = _page_dtype(q, "q"), q.shape, q.stride()
+    if len(shape) != 3 or strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]):
         raise ValueError("q must be [B, H_q, d] with contiguous heads")
-    return dtype, *q.shape, q.stride(0)
+    return dtype, *shape, strides[0]
 
 
 def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *, budget: int,
                  keep_first: int = 1, keep_last: int = 1, pages: torch.Tensor | None = None,
-                 lens: torch.Tensor | None = None):
+                 lens: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The `budget` pages of each (sequence, kv head) whose bounds allow the largest q . k (the first keep_first and
     last keep_last always): (pages int32 [B, H_kv, budget] of head pages, lens int32 [B, H_kv]), to be passed as
-    block_table and seq_lens to attend_pages or attend_decode."""
+    block_table and seq_lens to attend_pages or attend_decode.  workspace: scratch of 4 * B * H_kv * max_blocks bytes
+    (a call with few rows allocates it if it is not given)."""
     dtype, b, hq, d, q_stride = _q_rows(q)
     dev = q.device
     if bounds.dim() != 4:
@@ -671,50 +688,57 @@ def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
         pages = torch.empty((b, h, budget), dtype=torch.int32, device=dev)
     if lens is None:
         lens = torch.empty((b, h), dtype=torch.int32, device=dev)
-    i32 = torch.int32
-    a = SelectArgs(dtype, b, hq, h, d, block_table.shape[-1], n, budget, keep_first, keep_last, q.data_ptr(), q_stride,
+    i32, width = torch.int32, block_table.shape[-1]
+    a = SelectArgs(dtype, b, hq, h, d, width, n, budget, keep_first, keep_last, q.data_ptr(), q_stride,
                    _need(bounds, "bounds", q.dtype, (n, h, 2, d), dev),
-                   _need(block_table, "block_table", i32, (b, None), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
+                   _need(block_table, "block_table", i32, (b, width), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
                    _need(pages, "pages", i32, (b, h, budget), dev), _need(lens, "lens", i32, (b, h), dev))
-    _run_on(dev, "tq_select_pages", a)
+    if workspace is None:
+        nb = ctypes.c_size_t()
+        _run_on(dev, "tq_select_pages_workspace_bytes", LIB.tq_select_pages_workspace_bytes, a, ctypes.byref(nb))
+        if nb.value:
+            workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise TypeError(f"workspace must be on {dev}")
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.nbytes
+    _run_on(dev, "tq_select_pages", LIB.tq_select_pages, a)
     return pages, lens
 
 
-def _pool(t: torch.Tensor, name: str, shape, q):
-    """Pointer and page stride of a pool whose pages are contiguous but may lie apart (a half of a joint pool)."""
-    if t.dtype != q.dtype or t.device != q.device or t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)} with the dtype and device of q")
-    if t.stride()[1:] != (PAGE * shape[3], shape[3], 1):
-        raise ValueError(f"each page of {name} must be contiguous [H_kv, 16, d]")
-    return t.data_ptr(), t.stride(0)
+def _pool(t: torch.Tensor, name: str, q, device, page: tuple):
+    """Address and page stride of a pool whose pages are contiguous but may lie apart (a half of a joint pool)."""
+    strides = t.stride()
+    if t.dtype is not q.dtype or t.device != device:
+        raise TypeError(f"{name} must have the dtype and device of q")
+    if t.shape[1:] != page or strides[1:] != (page[1] * page[2], page[2], 1):
+        raise ValueError(f"{name} must be pages of contiguous {list(page)}, got {list(t.shape)} with strides {list(strides)}")
+    return t.data_ptr(), strides[0]
 
 
 def _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace) -> AttendPagesArgs:
     dtype, b, hq, d, q_stride = _q_rows(q)
     dev = q.device
-    if k_pool.dim() != 4 or k_pool.shape[2:] != (PAGE, d):
-        raise ValueError("k_pool must be [num_pages, H_kv, 16, d]")
     n, h = k_pool.shape[:2]
-    kp, k_page = _pool(k_pool, "k_pool", k_pool.shape, q)
-    vp, v_page = _pool(v_pool, "v_pool", k_pool.shape, q)
-    selected = block_table.dim() == 3
-    rows = (b, h) if selected else (b,)
-    return AttendPagesArgs(dtype, b, hq, h, d, block_table.shape[-1], n, int(selected), float(scale), q.data_ptr(),
-                           q_stride, kp, vp, k_page, v_page,
-                           _need(block_table, "block_table", torch.int32, (*rows, None), dev),
+    if v_pool.shape[0] != n:
+        raise ValueError("k_pool and v_pool must have the same number of pages")
+    kp, k_page = _pool(k_pool, "k_pool", q, dev, (h, PAGE, d))
+    vp, v_page = _pool(v_pool, "v_pool", q, dev, (h, PAGE, d))
+    rows = (b, h) if block_table.dim() == 3 else (b,)
+    width = block_table.shape[-1]
+    return AttendPagesArgs(dtype, b, hq, h, d, width, n, len(rows) - 1, scale, q.data_ptr(), q_stride, kp, vp, k_page,
+                           v_page, _need(block_table, "block_table", torch.int32, (*rows, width), dev),
                            _need(seq_lens, "seq_lens", torch.int32, rows, dev),
                            _need(out, "out", torch.float32, (b, hq, d), dev) if out is not None else None,
                            workspace.data_ptr() if workspace is not None else None,
-                           workspace.numel() * workspace.element_size() if workspace is not None else 0)
+                           workspace.nbytes if workspace is not None else 0)
 
 
 def attend_pages_workspace(q, k_pool, v_pool, block_table, seq_lens) -> torch.Tensor:
     """A workspace of the size tq_attend_pages_workspace_bytes asks for."""
     a = _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, 0.0, None, None)
     nb = ctypes.c_size_t()
-    with torch.cuda.device(q.device):
-        _check("tq_attend_pages_workspace_bytes",
-               LIB.tq_attend_pages_workspace_bytes(ctypes.byref(a), ctypes.byref(nb)))
+    _run_on(q.device, "tq_attend_pages_workspace_bytes", LIB.tq_attend_pages_workspace_bytes, a, ctypes.byref(nb))
     return torch.empty(nb.value, dtype=torch.uint8, device=q.device)
 
 
@@ -730,7 +754,7 @@ def attend_pages(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, bl
         workspace = attend_pages_workspace(q, k_pool, v_pool, block_table, seq_lens)
     elif workspace.device != q.device:
         raise TypeError(f"workspace must be on {q.device}")
-    _run_on(q.device, "tq_attend_pages",
+    _run_on(q.device, "tq_attend_pages", LIB.tq_attend_pages,
             _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace))
     return out
 
