@@ -559,13 +559,14 @@ typedef struct tq_attend_pages_args {
     const int32_t* block_table;/* device int32; entries past a row's length are not read */
     const int32_t* seq_lens;   /* device int32 (clamped to 0 .. max_blocks * 16) */
     float* out;                /* device float [batch][num_q_heads][head_dim] */
-    void* workspace;           /* device scratch (16-byte aligned); needs no initialisation, overwritten by every call */
+    void* workspace;           /* device scratch (16-byte aligned; may be NULL if none is needed); needs no
+                                  initialisation, overwritten by every call */
     size_t workspace_bytes;
 } tq_attend_pages_args;
 
 /*
  * tq_attend_pages_workspace_bytes -- bytes of workspace tq_attend_pages needs for these shapes on the current device
- * (never more than 8 MiB on a B200).  Only the shape fields are read.
+ * (never more than 8 MiB on a B200; 0 for table rows of up to 32 pages).  Only the shape fields are read.
  */
 tq_status tq_attend_pages_workspace_bytes(const tq_attend_pages_args* args, size_t* bytes);
 

@@ -215,6 +215,7 @@ constexpr int kSortRoom = 32768;       // keys that select_kernel's SCORED form 
 
 struct SelectPlan {
     bool scored;                       // the keys are computed by a grid of their own, through the workspace
+    int tile;                          // pages a CTA of that grid takes
     int room;                          // pages whose keys select_kernel keeps in shared memory
     size_t workspace_bytes;
 };
@@ -237,7 +238,11 @@ tq_status plan_select(const char* fn, const tq_select_args* a, SelectPlan* plan)
     const bool fits = query_smem(a->num_q_heads / a->num_kv_heads, a->head_dim) + static_cast<size_t>(even) * 8 <= kSelSmem;
     plan->scored = !fits || (rows < device_sms() && width > kScoreTile);
     plan->room = plan->scored ? (width < kSortRoom ? width : kSortRoom) : even;
-    TQ_NEED(rows * ((width + kScoreTile - 1) / kScoreTile) < (1ll << 31), TQ_ERR_UNSUPPORTED,
+    // two scoring CTAs to an SM with equal work, unless that leaves them little
+    int64_t tile = (rows * width + 2 * device_sms() - 1) / (2 * device_sms());
+    tile = (tile + 15) / 16 * 16;
+    plan->tile = static_cast<int>(tile < 64 ? 64 : (tile > kScoreTile ? kScoreTile : tile));
+    TQ_NEED(rows * ((width + plan->tile - 1) / plan->tile) < (1ll << 31), TQ_ERR_UNSUPPORTED,
             "%s: too many (sequence, kv head) rows for max_blocks=%d", fn, width);
     plan->workspace_bytes = plan->scored ? static_cast<size_t>(rows) * width * 4 : 0;
     return TQ_OK;
@@ -256,8 +261,9 @@ tq_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaSt
     // the selection itself does not depend on the type or the head size
     constexpr auto kern = select_kernel<__half, 64, true>;
     TQ_CUDA((prepare_kernel<kern>(kSortRoom * 4)), "tq_select_pages: cudaFuncSetAttribute");
-    const unsigned tiles = (p.width + kScoreTile - 1) / kScoreTile;
-    score_kernel<T, D><<<grid * tiles, kScoreThreads, query_smem(p.group, D), st>>>(p);
+    const unsigned tiles = (p.width + p.tile - 1) / p.tile;
+    TQ_CUDA((prepare_kernel<score_kernel<T, D>>(score_smem<D>(8))), "tq_select_pages: cudaFuncSetAttribute");
+    score_kernel<T, D><<<grid * tiles, kScoreThreads, score_smem<D>(p.group), st>>>(p);
     TQ_CUDA(cudaGetLastError(), "tq_select_pages: score launch");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -314,6 +320,7 @@ extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
     p.budget = a->budget;
     p.keep_first = a->keep_first;
     p.keep_last = a->keep_last;
+    p.tile = plan.tile;
     p.room = plan.room;
     p.keys = static_cast<uint32_t*>(a->workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -329,7 +336,11 @@ namespace {
 template <int D>
 constexpr int min_share() { return PagesCfg<D>::kRowCost + PagesCfg<D>::kWarps; }
 
+// Table rows of at most this many pages are not split: a second launch takes longer than a CTA needs for them.
+constexpr int kDirectPages = 32;
+
 struct PagesPlan {
+    bool direct;
     int ctas, rows_join;
     size_t meta_bytes, workspace_bytes;
 };
@@ -351,10 +362,15 @@ tq_status plan_attend_pages(const char* fn, const tq_attend_pages_args* a, Pages
     const int64_t want = (cost + least - 1) / least;
     TQ_NEED(cost < (1ll << 31), TQ_ERR_UNSUPPORTED, "%s: batch=%d with %d kv heads and max_blocks=%d holds 2^31 pages or more", fn,
             a->batch, a->num_kv_heads, a->max_blocks);
-    plan->ctas = static_cast<int>(want < slots ? want : slots);
-    // the join goes by rows if there are no more of them than shares
     const int rows = a->batch * a->num_kv_heads;
-    plan->rows_join = rows <= plan->ctas ? rows : 0;
+    plan->direct = a->max_blocks <= kDirectPages;
+    plan->ctas = plan->direct ? rows : static_cast<int>(want < slots ? want : slots);
+    // the join goes by rows if there are no more of them than shares
+    plan->rows_join = !plan->direct && rows <= plan->ctas ? rows : 0;
+    if (plan->direct) {
+        plan->meta_bytes = plan->workspace_bytes = 0;
+        return TQ_OK;
+    }
     plan->meta_bytes = static_cast<size_t>(plan->ctas) * sizeof(AttendPagesMeta);
     plan->workspace_bytes = plan->meta_bytes + static_cast<size_t>(plan->ctas) * 2 * (16 + 8 * d) * 4;
     return TQ_OK;
@@ -368,7 +384,7 @@ tq_status launch_attend_pages(AttendPagesParams& p, int ctas, cudaStream_t st) {
     TQ_CUDA((prepare_kernel<kern>(C::smem(8))), "tq_attend_pages: cudaFuncSetAttribute");
     kern<<<ctas, C::kThreads, C::smem(p.group), st>>>(p);
     TQ_CUDA(cudaGetLastError(), "tq_attend_pages: launch");
-    if (ctas > 1) {
+    if (!p.direct && ctas > 1) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -403,7 +419,7 @@ extern "C" tq_status tq_attend_pages(const tq_attend_pages_args* a, void* stream
     tq_status s = plan_attend_pages(fn, a, &plan);
     if (s != TQ_OK) return s;
     TQ_NEED(a->q && a->k_pool && a->v_pool && a->block_table && a->seq_lens && a->out, TQ_ERR_INVALID_ARG, "%s: NULL pointer in args", fn);
-    TQ_NEED(a->workspace && a->workspace_bytes >= plan.workspace_bytes, TQ_ERR_INVALID_ARG,
+    TQ_NEED(plan.workspace_bytes == 0 || (a->workspace && a->workspace_bytes >= plan.workspace_bytes), TQ_ERR_INVALID_ARG,
             "%s: workspace of %zu bytes required (got %zu)", fn, plan.workspace_bytes, a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
     TQ_NEED(aligned(a->q, 16) && aligned(a->k_pool, 16) && aligned(a->v_pool, 16) && aligned(a->out, 16) && aligned(a->workspace, 16),
             TQ_ERR_INVALID_ARG, "%s: q, k_pool, v_pool, out and workspace must be 16-byte aligned", fn);
@@ -441,6 +457,7 @@ extern "C" tq_status tq_attend_pages(const tq_attend_pages_args* a, void* stream
         p.k_page = a->k_page_stride;
         p.v_page = a->v_page_stride;
     }
+    p.direct = plan.direct;
     p.rows_join = plan.rows_join;
     // rows in many shares are joined by a CTA per head (or per few, so that the CTAs are resident together), those in
     // the few shares that many rows have by a CTA for 64 threads' worth of heads

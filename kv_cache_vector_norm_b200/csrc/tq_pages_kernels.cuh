@@ -380,12 +380,13 @@ struct SelectParams {
     int32_t* pages;                    // [B][H_kv][budget]
     int32_t* lens;                     // [B][H_kv]
     int heads, group, width, num_pages, budget, keep_first, keep_last;
+    int tile;                          // pages a CTA of score_kernel scores
     int room;                          // pages whose keys (and, unless SCORED, ids) select_kernel's shared memory holds
     uint32_t* keys;                    // [B][H_kv][width]: keys of score_kernel (select_kernel's SCORED form)
 };
 
 constexpr int kScoreThreads = 256;     // threads that score pages together: a CTA of score_kernel, or of select_kernel
-constexpr int kScoreTile = 256;        // pages a CTA of score_kernel scores
+constexpr int kScoreTile = 256;        // pages a CTA of score_kernel scores, at most
 constexpr int kSortThreads = 1024;     // threads of select_kernel's SCORED form
 
 inline __host__ __device__ size_t query_smem(int group, int d) { return static_cast<size_t>(group) * d * 8; }
@@ -404,8 +405,8 @@ __device__ __forceinline__ void load_query(const SelectParams& p, int b, int h, 
     }
 }
 
-// Keys (order-preserving bits of the scores) of pages p0 .. p0 + cnt - 1 of a row of nb pages, whose ids are in shared
-// memory, by the whole block.
+// One round of scoring: keys (order-preserving bits of the scores) of pages base .. base + U - 1 for each lane group of
+// d / 8 lanes, of the cnt pages from p0 on of a row of nb pages.  lo16, hi16: this lane's 8 channels of the bounds.
 //
 // The score of a page is max over the group's query heads of U_g = sum_c max(q_gc lo_c, q_gc hi_c), which is at least
 // q_g . k for every key in the page.  With lo <= hi the larger product is (q > 0 ? q hi : q lo), computed as two
@@ -414,80 +415,70 @@ __device__ __forceinline__ void load_query(const SelectParams& p, int b, int h, 
 // operator (a lane's 8 channels as an even and an odd chain, then lanes i and i + half), so that the choice of pages
 // can be reproduced bit for bit; it also rules out the tensor cores, whose order is not defined.
 template <typename T, int D, int U>
-__device__ __forceinline__ void score_pages(const SelectParams& p, int h, int nb, int p0, int cnt, const int32_t* ids,
-                                            const float* qp, const float* qn, uint32_t* keys) {
+__device__ __forceinline__ void score_round(const SelectParams& p, const float4* qp4, const float4* qn4, const uint4 (&lo16)[U],
+                                            const uint4 (&hi16)[U], int nb, int p0, int cnt, int base, const int32_t* ids,
+                                            uint32_t* keys) {
     constexpr int LP = D / 8;                            // lanes per page
-    constexpr int GW = 32 / LP;                          // lane groups per warp
     static_assert(U == 2 || U == 4, "the reduction below spreads two or four pages over the lanes of a group");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LP;
+    constexpr int kHeads = U == 4 ? 2 : 1;               // heads in flight: one's products run under the other's shuffles
+    const int l = threadIdx.x % LP;
     const bool upper = (l & (LP / 2)) != 0, odd = (l & (LP / 4)) != 0;
-    const float4* qp4 = reinterpret_cast<const float4*>(qp) + l;
-    const float4* qn4 = reinterpret_cast<const float4*>(qn) + l;
-    const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + l * 8;
-    const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
-    constexpr int kStep = (kScoreThreads / 32) * GW * U;
-    for (int base = (warp * GW + lane / LP) * U; base - (lane / LP) * U < cnt; base += kStep) {
-        float2 lo[U][4], hi[U][4];
+    float2 lo[U][4], hi[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t aw[4] = {lo16[u].x, lo16[u].y, lo16[u].z, lo16[u].w};
+        const uint32_t cw[4] = {hi16[u].x, hi16[u].y, hi16[u].z, hi16[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[u][i] = Pair<T>::floats(aw[i]);
+            hi[u][i] = Pair<T>::floats(cw[i]);
+        }
+    }
+    float best = -INFINITY;
+#pragma unroll kHeads
+    for (int g = 0; g < p.group; ++g) {
+        const float4 p0v = qp4[g * (D / 4)], p1v = qp4[g * (D / 4) + LP];
+        const float4 n0v = qn4[g * (D / 4)], n1v = qn4[g * (D / 4) + LP];
+        const float2 pq[4] = {{p0v.x, p0v.y}, {p0v.z, p0v.w}, {p1v.x, p1v.y}, {p1v.z, p1v.w}};
+        const float2 nq[4] = {{n0v.x, n0v.y}, {n0v.z, n0v.w}, {n1v.x, n1v.y}, {n1v.z, n1v.w}};
+        float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int id = base + u < cnt ? ids[base + u] : -1;
-            uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
-            if (id >= 0 && id < p.num_pages) {
-                const T* src = bounds + id * page_stride;
-                a = __ldg(reinterpret_cast<const uint4*>(src));
-                c = __ldg(reinterpret_cast<const uint4*>(src + D));
-            }
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
+            float2 acc = __fmul2_rn(pq[0], hi[u][0]);
+            acc = __ffma2_rn(nq[0], lo[u][0], acc);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[u][i] = Pair<T>::floats(aw[i]);
-                hi[u][i] = Pair<T>::floats(cw[i]);
+            for (int i = 1; i < 4; ++i) {
+                acc = __ffma2_rn(pq[i], hi[u][i], acc);
+                acc = __ffma2_rn(nq[i], lo[u][i], acc);
             }
+            v[u] = acc.x + acc.y;
         }
-        float best = -INFINITY;
-        for (int g = 0; g < p.group; ++g) {
-            const float4 p0v = qp4[g * (D / 4)], p1v = qp4[g * (D / 4) + LP];
-            const float4 n0v = qn4[g * (D / 4)], n1v = qn4[g * (D / 4) + LP];
-            const float2 pq[4] = {{p0v.x, p0v.y}, {p0v.z, p0v.w}, {p1v.x, p1v.y}, {p1v.z, p1v.w}};
-            const float2 nq[4] = {{n0v.x, n0v.y}, {n0v.z, n0v.w}, {n1v.x, n1v.y}, {n1v.z, n1v.w}};
-            float v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc = __ffma2_rn(pq[i], hi[u][i], acc);
-                    acc = __ffma2_rn(nq[i], lo[u][i], acc);
-                }
-                v[u] = acc.x + acc.y;
-            }
-            // lanes i and i + LP/2 add up, the upper half going on with one half of the pages and the lower with the
-            // other; then quarters
-            float s;
-            if constexpr (U == 4) {
-                const float k0 = upper ? v[2] : v[0], k1 = upper ? v[3] : v[1];
-                const float g0 = upper ? v[0] : v[2], g1 = upper ? v[1] : v[3];
-                const float w0 = k0 + __shfl_xor_sync(0xffffffffu, g0, LP / 2);
-                const float w1 = k1 + __shfl_xor_sync(0xffffffffu, g1, LP / 2);
-                s = (odd ? w1 : w0) + __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, LP / 4);
-            } else {
-                s = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], LP / 2);
-                s += __shfl_xor_sync(0xffffffffu, s, LP / 4);
-            }
-#pragma unroll
-            for (int o = LP / 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            // a NaN sum must not hide behind another head's number
-            best = (s > best || s != s) ? s : best;
+        // lanes i and i + LP/2 add up, the upper half going on with one half of the pages and the lower with the
+        // other; then quarters
+        float s;
+        if constexpr (U == 4) {
+            const float k0 = upper ? v[2] : v[0], k1 = upper ? v[3] : v[1];
+            const float g0 = upper ? v[0] : v[2], g1 = upper ? v[1] : v[3];
+            const float w0 = k0 + __shfl_xor_sync(0xffffffffu, g0, LP / 2);
+            const float w1 = k1 + __shfl_xor_sync(0xffffffffu, g1, LP / 2);
+            s = (odd ? w1 : w0) + __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, LP / 4);
+        } else {
+            s = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], LP / 2);
+            s += __shfl_xor_sync(0xffffffffu, s, LP / 4);
         }
-        const int j = base + (U == 4 ? (upper ? 2 : 0) + (odd ? 1 : 0) : (upper ? 1 : 0));
-        if ((l & (LP / U - 1)) == 0 && j < cnt) {
-            const int at = p0 + j, id = ids[j];
-            uint32_t bits = __float_as_uint(best + 0.f);             // -0 counts as 0
-            bits = (bits >> 31) ? ~bits : bits | 0x80000000u;
-            if (best != best || id < 0 || id >= p.num_pages) bits = 0u;
-            if (at < p.keep_first || at >= nb - p.keep_last) bits = 0xffffffffu;
-            keys[j] = bits;
-        }
+#pragma unroll
+        for (int o = LP / 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        // a sum that is not a number does not hide behind another head's
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(best) : "f"(s));
+    }
+    const int j = base + (U == 4 ? (upper ? 2 : 0) + (odd ? 1 : 0) : (upper ? 1 : 0));
+    if ((l & (LP / U - 1)) == 0 && j < cnt) {
+        const int at = p0 + j, id = ids[j];
+        uint32_t bits = __float_as_uint(best + 0.f);                 // -0 counts as 0
+        bits = (bits >> 31) ? ~bits : bits | 0x80000000u;
+        if (best != best || id < 0 || id >= p.num_pages) bits = 0u;
+        if (at < p.keep_first || at >= nb - p.keep_last) bits = 0xffffffffu;
+        keys[j] = bits;
     }
 }
 
@@ -497,26 +488,67 @@ __device__ __forceinline__ int64_t select_len(const SelectParams& p, int b) {
 }
 
 // Keys of a call with few rows, where a CTA per row would leave most of the GPU idle: a CTA per row and kScoreTile
-// pages.  Four pages per lane group share each read of the query from shared memory, which otherwise is the limit.
+// pages.  Four pages per lane group share each read of the query from shared memory.  With the registers that takes
+// there are 16 warps on an SM, too few to hide the loads, so each lane's next bounds are copied (cp.async) to a slot
+// that only it reads while it works on the ones before.
+template <int D>
+constexpr int score_smem(int group) { return static_cast<int>(query_smem(group, D)) + 2 * 4 * 2 * 16 * kScoreThreads; }
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectParams p) {
+    constexpr int U = 4, LP = D / 8, GW = 32 / LP;
+    constexpr int kRound = (kScoreThreads / 32) * GW * U;            // pages per round of the block
     extern __shared__ __align__(16) uint8_t smem[];
     float* qp = reinterpret_cast<float*>(smem);
     float* qn = qp + p.group * D;
+    uint4* slots = reinterpret_cast<uint4*>(qn + p.group * D) + threadIdx.x;   // [2][U][lo, hi][threads]
     __shared__ int32_t s_ids[kScoreTile];
     static_assert(kScoreTile == kScoreThreads, "a thread per page id");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tiles = (p.width + kScoreTile - 1) / kScoreTile;
+    const int tiles = (p.width + p.tile - 1) / p.tile;
     const int row = blockIdx.x / tiles, b = row / p.heads, h = row - b * p.heads;
     const int64_t len = select_len(p, b);
-    const int p0 = (blockIdx.x - row * tiles) * kScoreTile;
+    const int p0 = (blockIdx.x - row * tiles) * p.tile;
     load_query<T, D>(p, b, h, qp, qn);
     if (p0 + threadIdx.x < p.width) s_ids[threadIdx.x] = p.table[static_cast<int64_t>(b) * p.width + p0 + threadIdx.x];
     const int nb = static_cast<int>((len + kPage - 1) / kPage);
     if (p0 >= nb || nb <= p.budget) return;
-    const int cnt = nb - p0 < kScoreTile ? nb - p0 : kScoreTile;
+    const int cnt = nb - p0 < p.tile ? nb - p0 : p.tile;
     __syncthreads();
-    score_pages<T, D, 4>(p, h, nb, p0, cnt, s_ids, qp, qn, p.keys + static_cast<int64_t>(row) * p.width + p0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LP;
+    const float4* qp4 = reinterpret_cast<const float4*>(qp) + l;
+    const float4* qn4 = reinterpret_cast<const float4*>(qn) + l;
+    const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + l * 8;
+    const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
+    const int w0 = warp * GW * U;                        // the warp's first page of a round
+    auto fetch = [&](int round) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = round * kRound + w0 + lane / LP * U + u;
+            const int id = j < cnt ? s_ids[j] : -1;
+            if (id >= 0 && id < p.num_pages) {           // else the slot's old contents are scored and not used
+                const T* src = bounds + id * page_stride;
+                const uint32_t dst = smem_u32(slots + (round & 1) * U * 2 * kScoreThreads + u * 2 * kScoreThreads);
+                cp_async16(dst, src);
+                cp_async16(dst + 16 * kScoreThreads, src + D);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0);
+    uint32_t* keys = p.keys + static_cast<int64_t>(row) * p.width + p0;
+    for (int round = 0; round * kRound + w0 < cnt; ++round) {
+        fetch(round + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        uint4 lo[U], hi[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            lo[u] = slots[((round & 1) * U + u) * 2 * kScoreThreads];
+            hi[u] = slots[((round & 1) * U + u) * 2 * kScoreThreads + kScoreThreads];
+        }
+        score_round<T, D, U>(p, qp4, qn4, lo, hi, nb, p0, cnt, round * kRound + w0 + lane / LP * U, s_ids, keys);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // The `budget` best pages of one (sequence, kv head), by one CTA.  SCORED: score_kernel computes the keys, and this
@@ -559,28 +591,76 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
         }
         return;
     }
+    // Thread t looks after pages j0 .. j1 - 1.  Up to kHeld of them stay in registers; the keys of longer rows are read
+    // again in every pass (from shared memory, or from L2 if they do not fit there).
+    constexpr int kHeld = 8;
+    const int chunk = (nb + NT - 1) / NT;
+    const int j0 = tid * chunk < nb ? tid * chunk : nb, j1 = j0 + chunk < nb ? j0 + chunk : nb;
+    const bool held = chunk <= kHeld;
     const uint32_t* keys = room;
+    uint32_t key[kHeld];
+    int id[kHeld];
     if constexpr (SCORED) {
+        if (held) {                                      // before the scores are there
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) id[i] = j0 + i < j1 ? table[j0 + i] : -1;
+        }
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t* src = p.keys + static_cast<int64_t>(row) * p.width;
-        if (nb <= p.room) {
+        if (held || nb > p.room) {
+            keys = src;
+        } else {
 #pragma unroll 4
             for (int j = tid; j < nb; j += NT) room[j] = __ldcg(src + j);
-        } else {
-            keys = src;                                  // a very long sequence: the passes read the L2 cache
         }
     } else {
         __syncthreads();
-        score_pages<T, D, 2>(p, h, nb, 0, nb, ids, qp, qn, room);
+        constexpr int U = 2, LP = D / 8, GW = 32 / LP;
+        const int l = lane % LP;
+        const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + l * 8;
+        const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
+        for (int w0 = warp * GW * U; w0 < nb; w0 += NW * GW * U) {
+            const int base = w0 + lane / LP * U;
+            uint4 lo[U], hi[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int id = base + u < nb ? ids[base + u] : -1;
+                lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (id >= 0 && id < p.num_pages) {
+                    lo[u] = __ldg(reinterpret_cast<const uint4*>(bounds + id * page_stride));
+                    hi[u] = __ldg(reinterpret_cast<const uint4*>(bounds + id * page_stride + D));
+                }
+            }
+            score_round<T, D, U>(p, reinterpret_cast<const float4*>(qp) + l, reinterpret_cast<const float4*>(qn) + l, lo, hi, nb,
+                                 0, nb, base, ids, room);
+        }
     }
     __syncthreads();
-    // ---- the range of the keys that compete
-    const int c0 = p.keep_first, c1 = nb - p.keep_last;  // pages c0 .. c1 - 1
-    uint32_t least = 0xffffffffu, most = 0u;
-    for (int j = c0 + tid; j < c1; j += NT) {
-        least = min(least, keys[j]);
-        most = max(most, keys[j]);
+    if (held) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            key[i] = j0 + i < j1 ? (SCORED ? __ldcg(keys + j0 + i) : keys[j0 + i]) : 0u;
+            if (!SCORED) id[i] = j0 + i < j1 ? ids[j0 + i] : -1;
+        }
     }
+    auto each = [&](auto f) {                            // f(page, its key, its id if it is held) for the thread's pages
+        if (held) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                if (j0 + i < j1) f(j0 + i, key[i], id[i]);
+        } else {
+            for (int j = j0; j < j1; ++j) f(j, keys[j], 0);
+        }
+    };
+    // ---- the range of the keys that compete: pages c0 .. c1 - 1
+    const int c0 = p.keep_first, c1 = nb - p.keep_last < j1 ? nb - p.keep_last : j1;
+    uint32_t least = 0xffffffffu, most = 0u;
+    each([&](int j, uint32_t k, int) {
+        if (j >= c0 && j < c1) {
+            least = min(least, k);
+            most = max(most, k);
+        }
+    });
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) {
@@ -590,20 +670,18 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     __syncthreads();
     least = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0xffffffffu);
     most = __reduce_max_sync(0xffffffffu, lane < NW ? s_warp2[lane] : 0u);
-    // ---- the threshold: keys above `least` + 2^bits - 1 are in, those below `least` out
-    uint32_t need = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);   // of the keys in between
+    // ---- the threshold: of the keys from `bound` to `bound` + 2^bits - 1, the `need` largest are in; all above are
+    uint32_t need = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);
     int bits = 32 - __clz(static_cast<int>(most - least));
-    bool whole = need == 0;                              // nothing or everything in between is in
-    uint32_t bound = need == 0 ? 0xffffffffu : least;    // whole: keys from `bound` on are in
+    bool whole = need == 0;                              // everything from `bound` on is in
+    uint32_t bound = need == 0 ? 0xffffffffu : least;    // (need 0: nothing but the pages kept in any case)
     for (int pass = 0; !whole; ++pass) {
         const int shift = bits > 8 ? bits - 8 : 0;
         const uint32_t width = bits == 32 ? 0xffffffffu : (1u << bits) - 1u;
         uint32_t* hist = s_hist[pass & 1];
-#pragma unroll 4
-        for (int j = c0 + tid; j < c1; j += NT) {
-            const uint32_t off = keys[j] - bound;
-            if (off <= width) atomicAdd(&hist[off >> shift], 1u);
-        }
+        each([&](int j, uint32_t k, int) {
+            if (j >= c0 && j < c1 && k - bound <= width) atomicAdd(&hist[(k - bound) >> shift], 1u);
+        });
         __syncthreads();
         // thread t takes bin 255 - t, so that an inclusive scan counts the keys from the largest bin down
         uint32_t c = 0, incl = 0;
@@ -634,40 +712,40 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
         bits = shift;
         if (shift == 0) break;
     }
-    // in: keys above `bound` (whole: from it on), the first `need` of those equal to it, and the pages kept in any case
+    // ---- the list: keys from `from` on, and the first `need` of those equal to `bound`
     const uint32_t from = whole ? bound : bound + 1;     // bound < 2^32 - 1: that key is of pages kept in any case
     if (whole) need = 0;
-    const int chunk = ((nb + NW - 1) / NW + 31) & ~31;   // pages of a warp
-    const int j0 = warp * chunk, j1 = j0 + chunk < nb ? j0 + chunk : nb;
     uint32_t n_in = 0, n_tie = 0;
-    for (int j = j0; j < j1; j += 32) {
-        const bool there = j + lane < j1;
-        const uint32_t key = there ? keys[j + lane] : 0u;
-        n_in += __popc(__ballot_sync(0xffffffffu, there && key >= from));
-        n_tie += __popc(__ballot_sync(0xffffffffu, there && key < from && key == bound));
+    each([&](int, uint32_t k, int) {
+        n_in += k >= from ? 1u : 0u;
+        n_tie += k < from && k == bound ? 1u : 0u;
+    });
+    uint32_t in_before = n_in, ties_before = n_tie;      // in the threads before this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t a = __shfl_up_sync(0xffffffffu, in_before, o), t = __shfl_up_sync(0xffffffffu, ties_before, o);
+        if (lane >= o) {
+            in_before += a;
+            ties_before += t;
+        }
     }
     __syncthreads();                                     // the sums before have been read
-    if (lane == 0) {
-        s_warp[warp] = n_in;
-        s_warp2[warp] = n_tie;
+    if (lane == 31) {
+        s_warp[warp] = in_before;
+        s_warp2[warp] = ties_before;
     }
     __syncthreads();
-    uint32_t in_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
-    uint32_t ties_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u);
-    const unsigned below = (1u << lane) - 1u;
-    for (int j = j0; j < j1; j += 32) {
-        const bool there = j + lane < j1;
-        const uint32_t key = there ? keys[j + lane] : 0u;
-        const bool in = there && key >= from, tie = there && key < from && key == bound;
-        const unsigned mi = __ballot_sync(0xffffffffu, in), mt = __ballot_sync(0xffffffffu, tie);
-        const uint32_t i_at = in_before + __popc(mi & below), t_at = ties_before + __popc(mt & below);
-        if (in || (tie && t_at < need)) {
-            const int id = SCORED ? table[j + lane] : ids[j + lane];
-            out[i_at + (t_at < need ? t_at : need)] = (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h;
+    in_before += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u) - n_in;
+    ties_before += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u) - n_tie;
+    each([&](int j, uint32_t k, int page) {
+        const bool in = k >= from, tie = !in && k == bound;
+        if (in || (tie && ties_before < need)) {
+            const int e = held ? page : (SCORED ? table[j] : ids[j]);
+            out[in_before + (ties_before < need ? ties_before : need)] = (e < 0 || e >= p.num_pages) ? -1 : e * p.heads + h;
         }
-        in_before += __popc(mi);
-        ties_before += __popc(mt);
-    }
+        in_before += in ? 1u : 0u;
+        ties_before += tie ? 1u : 0u;
+    });
 }
 
 // -------------------------------------------------------------------- attention over uncompressed pages
@@ -685,6 +763,7 @@ struct AttendPagesParams {
     int units, mult;                   // table rows, and kv heads that share a table row (1 for selections)
     int width, num_ids, heads, group;
     int min_share;                     // what a CTA takes at least
+    bool direct;                       // one CTA per row: nothing is cut, nothing joined
     int rows_join;                     // rows (units * mult) if the join goes by rows, else 0
     int join_heads;                    // heads that one CTA of the join takes
     float scale_log2;
@@ -814,7 +893,8 @@ __device__ __forceinline__ void advance(const AttendPagesParams& p, PageCursor& 
 // all pages of the call, in the order (table row, kv head, page), are cut into shares of equal cost, one per resident
 // CTA, whatever the lengths of the sequences are.  A share covers parts of one or several rows (a row: one sequence
 // and kv head with its query heads, whose own cost counts as kRowCost pages); a row that lies inside one share is
-// finished there, and attend_pages_join_kernel joins the others.  The running maximum and sum (fp32) make the split exact up to rounding.
+// finished there, and attend_pages_join_kernel joins the others.  Calls with short table rows take a CTA per row and
+// need no join.  The running maximum and sum (fp32) make the split exact up to rounding.
 //
 // Warp w of a CTA takes pages w, w + 4, ... of the share and keeps kStages of them in flight in its own ring of
 // shared memory with 16-byte cp.async copies, so no warp waits for another until a row ends.  16-byte chunk c of a
@@ -838,35 +918,9 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
     const int gid = lane >> 2, tig = lane & 3;
     const int G = p.group;
 
-    // ---- this CTA's share.  Thread t looks at units t * per .. t * per + per - 1.
-    auto unit_cost = [&](int u) -> int {                 // of each of the unit's rows
-        const int n = unit_pages(p, u);
-        return n ? n + C::kRowCost : 0;
-    };
-    const int per = (p.units + C::kThreads - 1) / C::kThreads;
-    const int u0 = tid * per, u1 = u0 + per < p.units ? u0 + per : p.units;
-    int own = 0;
-#pragma unroll 4
-    for (int u = u0; u < u1; ++u) own += unit_cost(u);
-    int incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-    }
-    if (lane == 31) s_setup[warp] = incl;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-        if (w < warp) incl += s_setup[w];
-        total += s_setup[w];
-    }
-    total *= p.mult;
-    int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-    if (share < p.min_share) share = p.min_share;
-    // past the last share x0 may pass 2^31: unsigned
-    const unsigned start = blockIdx.x * static_cast<unsigned>(share);
+    // ---- this CTA's share
+    int x0 = 0, x1, share = INT_MAX;
+    PageCursor seg;                                      // the first page at or behind x0
     auto write_zeros = [&]() {                           // rows without a token are nobody's page
         for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
             if (unit_pages(p, u) == 0) {
@@ -877,40 +931,80 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
             }
         }
     };
-    if (start >= static_cast<unsigned>(total)) {
-        if (!p.rows_join && tid == 0) p.meta[blockIdx.x].row = -1;
-        write_zeros();
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        return;
-    }
-    const int x0 = static_cast<int>(start), x1 = total - x0 < share ? total : x0 + share;
-    {
-        int begin = (incl - own) * p.mult;
-        if (x0 >= begin && x0 < incl * p.mult) {         // one thread: its units are read again
-            for (int u = u0; u < u1; ++u) {
-                const int cost = unit_cost(u), end = begin + cost * p.mult;
-                if (x0 < end) {
-                    s_setup[C::kWarps] = u;
-                    s_setup[C::kWarps + 1] = x0 - begin;
-                    s_setup[C::kWarps + 2] = cost;
-                    break;
+    if (p.direct) {
+        seg.x = seg.pg = 0;
+        seg.unit = blockIdx.x / p.mult;
+        seg.m = blockIdx.x - seg.unit * p.mult;
+        seg.pages = x1 = unit_pages(p, seg.unit);
+        if (x1 == 0) {
+            for (int i = tid; i < G * D; i += C::kThreads) p.out[static_cast<int64_t>(blockIdx.x) * G * D + i] = 0.f;
+            return;
+        }
+    } else {
+        // thread t looks at units t * per .. t * per + per - 1
+        auto unit_cost = [&](int u) -> int {                 // of each of the unit's rows
+            const int n = unit_pages(p, u);
+            return n ? n + C::kRowCost : 0;
+        };
+        const int per = (p.units + C::kThreads - 1) / C::kThreads;
+        const int u0 = tid * per, u1 = u0 + per < p.units ? u0 + per : p.units;
+        int own = 0;
+    #pragma unroll 4
+        for (int u = u0; u < u1; ++u) own += unit_cost(u);
+        int incl = own;
+    #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        if (lane == 31) s_setup[warp] = incl;
+        __syncthreads();
+        int total = 0;
+    #pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+            if (w < warp) incl += s_setup[w];
+            total += s_setup[w];
+        }
+        total *= p.mult;
+        share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+        if (share < p.min_share) share = p.min_share;
+        // past the last share x0 may pass 2^31: unsigned
+        const unsigned start = blockIdx.x * static_cast<unsigned>(share);
+        if (start >= static_cast<unsigned>(total)) {
+            if (!p.rows_join && tid == 0) p.meta[blockIdx.x].row = -1;
+            write_zeros();
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            return;
+        }
+        x0 = static_cast<int>(start);
+        x1 = total - x0 < share ? total : x0 + share;
+        {
+            int begin = (incl - own) * p.mult;
+            if (x0 >= begin && x0 < incl * p.mult) {         // one thread: its units are read again
+                for (int u = u0; u < u1; ++u) {
+                    const int cost = unit_cost(u), end = begin + cost * p.mult;
+                    if (x0 < end) {
+                        s_setup[C::kWarps] = u;
+                        s_setup[C::kWarps + 1] = x0 - begin;
+                        s_setup[C::kWarps + 2] = cost;
+                        break;
+                    }
+                    begin = end;
                 }
-                begin = end;
             }
         }
+        __syncthreads();
+        {
+            const int off = s_setup[C::kWarps + 1], cost = s_setup[C::kWarps + 2];
+            seg.unit = s_setup[C::kWarps];
+            seg.pages = cost - C::kRowCost;
+            seg.m = off / cost;
+            const int in_row = off - seg.m * cost;
+            seg.pg = in_row < C::kRowCost ? 0 : in_row - C::kRowCost;
+            seg.x = x0 - in_row + C::kRowCost + seg.pg;
+        }
+        __syncthreads();                                     // the rows' results may overwrite the set-up words
     }
-    __syncthreads();
-    PageCursor seg;                                      // the first page at or behind x0
-    {
-        const int off = s_setup[C::kWarps + 1], cost = s_setup[C::kWarps + 2];
-        seg.unit = s_setup[C::kWarps];
-        seg.pages = cost - C::kRowCost;
-        seg.m = off / cost;
-        const int in_row = off - seg.m * cost;
-        seg.pg = in_row < C::kRowCost ? 0 : in_row - C::kRowCost;
-        seg.x = x0 - in_row + C::kRowCost + seg.pg;
-    }
-    __syncthreads();                                     // the rows' results may overwrite the set-up words
 
     // ---- the copy ring
     const T* k_pool = static_cast<const T*>(p.k_pool);
@@ -963,8 +1057,8 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         next_m = ld.m;
     }
     // while the first pages are on their way
-    write_zeros();
-    if (!p.rows_join && tid == 0) {
+    if (!p.direct) write_zeros();
+    if (!p.direct && !p.rows_join && tid == 0) {
         // the row that crosses into this share, if this is its first crossing
         const int row_begin = seg.x - seg.pg, first = row_begin / share;
         AttendPagesMeta m;

@@ -706,24 +706,23 @@ def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     return pages, lens
 
 
-def _pool(t: torch.Tensor, name: str, q, device, page: tuple):
+def _pool(t: torch.Tensor, name: str, dtype, device, shape: tuple):
     """Address and page stride of a pool whose pages are contiguous but may lie apart (a half of a joint pool)."""
-    strides = t.stride()
-    if t.dtype is not q.dtype or t.device != device:
+    if t.dtype is not dtype or t.device != device:
         raise TypeError(f"{name} must have the dtype and device of q")
-    if t.shape[1:] != page or strides[1:] != (page[1] * page[2], page[2], 1):
-        raise ValueError(f"{name} must be pages of contiguous {list(page)}, got {list(t.shape)} with strides {list(strides)}")
-    return t.data_ptr(), strides[0]
+    page, head, row, unit = t.stride() if t.shape == shape else (0, 0, 0, 0)
+    if unit != 1 or row != shape[3] or head != PAGE * row:
+        raise ValueError(f"{name} must be {list(shape)}, each page contiguous; got {list(t.shape)}, strides {list(t.stride())}")
+    return t.data_ptr(), page
 
 
 def _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace) -> AttendPagesArgs:
     dtype, b, hq, d, q_stride = _q_rows(q)
     dev = q.device
     n, h = k_pool.shape[:2]
-    if v_pool.shape[0] != n:
-        raise ValueError("k_pool and v_pool must have the same number of pages")
-    kp, k_page = _pool(k_pool, "k_pool", q, dev, (h, PAGE, d))
-    vp, v_page = _pool(v_pool, "v_pool", q, dev, (h, PAGE, d))
+    shape, qt = (n, h, PAGE, d), q.dtype
+    kp, k_page = _pool(k_pool, "k_pool", qt, dev, shape)
+    vp, v_page = _pool(v_pool, "v_pool", qt, dev, shape)
     rows = (b, h) if block_table.dim() == 3 else (b,)
     width = block_table.shape[-1]
     return AttendPagesArgs(dtype, b, hq, h, d, width, n, len(rows) - 1, scale, q.data_ptr(), q_stride, kp, vp, k_page,

@@ -44,7 +44,7 @@ def select_args(**kw):
 def attend_args(**kw):
     d = kw.get("head_dim", 128)
     return filled(tq.AttendPagesArgs, **{**dict(dtype=tq.TQ_F16, batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128,
-                                                max_blocks=9, num_pages=64, selected=0, q_stride=1024, k_page_stride=32 * d,
+                                                max_blocks=90, num_pages=64, selected=0, q_stride=1024, k_page_stride=32 * d,
                                                 v_page_stride=32 * d, workspace_bytes=1 << 23), **kw})
 
 
@@ -107,7 +107,7 @@ def test_workspace_stays_small(d):
     for kw in (dict(batch=1, max_blocks=1), dict(batch=64, max_blocks=256), dict(batch=1, num_kv_heads=1, max_blocks=1 << 20)):
         a = attend_args(head_dim=d, **kw)
         assert tq.LIB.tq_attend_pages_workspace_bytes(ctypes.byref(a), ctypes.byref(nb)) == tq.TQ_OK
-        assert 0 < nb.value <= 8 << 20
+        assert (kw["max_blocks"] > 32) == (nb.value > 0) and nb.value <= 8 << 20
 
 
 def test_binding_checks_tensors():
