@@ -56,6 +56,23 @@ cudaError_t prepare_kernel(int smem) {
     return e;
 }
 
+// Launch a kernel as a programmatic dependent of the work before it (see begin_dependent).
+template <typename P, typename... Rest>
+cudaError_t launch(void (*kernel)(P, Rest...), unsigned grid_x, unsigned grid_y, int threads, size_t smem, cudaStream_t st,
+                   const P& p, Rest... rest) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid_x, grid_y);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, rest...);
+}
+
 tq_status check_heads(const char* fn, int batch, int hq, int hkv) {
     TQ_NEED(batch >= 1 && hq >= 1 && hkv >= 1, TQ_ERR_INVALID_ARG, "%s: batch, num_q_heads, num_kv_heads must be >= 1", fn);
     TQ_NEED(hq % hkv == 0, TQ_ERR_INVALID_ARG, "%s: num_q_heads=%d is not a multiple of num_kv_heads=%d", fn, hq, hkv);
@@ -127,23 +144,12 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // a decode step's few slots are written by the planning CTA itself, a prefill's by a grid of their own
     const bool one = a->max_tokens <= 1024;
-    if (a->batch <= 256 && one)
-        plan_kernel<256><<<1, 256, 0, st>>>(p, one);
-    else
-        plan_kernel<kPlanThreads><<<1, kPlanThreads, 0, st>>>(p, one);
-    TQ_CUDA(cudaGetLastError(), "tq_plan_pages: launch");
-    if (!one) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>((a->max_tokens + kSlotTile - 1) / kSlotTile));
-        cfg.blockDim = dim3(kSlotTile);
-        cfg.stream = st;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        TQ_CUDA(cudaLaunchKernelEx(&cfg, plan_slots_kernel, p), "tq_plan_pages: slot launch");
-    }
+    TQ_CUDA(a->batch <= 256 && one ? launch(plan_kernel<256>, 1, 1, 256, 0, st, p, one)
+                                   : launch(plan_kernel<kPlanThreads>, 1, 1, kPlanThreads, 0, st, p, one),
+            "tq_plan_pages: launch");
+    if (!one)
+        TQ_CUDA(launch(plan_slots_kernel, static_cast<unsigned>((a->max_tokens + kSlotTile - 1) / kSlotTile), 1, kSlotTile, 0, st, p),
+                "tq_plan_pages: slot launch");
     return TQ_OK;
 }
 
@@ -155,11 +161,8 @@ template <typename T, int D>
 tq_status launch_append(const AppendParams& p, cudaStream_t st) {
     const int64_t warps = (p.n + p.tile - 1) / p.tile * p.heads;
     const unsigned grid = static_cast<unsigned>((warps + kAppendWarps - 1) / kAppendWarps);
-    if (p.v_pool)
-        append_kernel<T, D, true><<<grid, 32 * kAppendWarps, 0, st>>>(p);
-    else
-        append_kernel<T, D, false><<<grid, 32 * kAppendWarps, 0, st>>>(p);
-    TQ_CUDA(cudaGetLastError(), "tq_append_pages: launch");
+    TQ_CUDA(launch(p.v_pool ? append_kernel<T, D, true> : append_kernel<T, D, false>, grid, 1, 32 * kAppendWarps, 0, st, p),
+            "tq_append_pages: launch");
     return TQ_OK;
 }
 
@@ -254,8 +257,8 @@ tq_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaSt
     if (!scored) {
         constexpr auto kern = select_kernel<T, D, false>;
         TQ_CUDA((prepare_kernel<kern>(kSelSmem)), "tq_select_pages: cudaFuncSetAttribute");
-        kern<<<grid, kScoreThreads, query_smem(p.group, D) + static_cast<size_t>(p.room) * 8, st>>>(p);
-        TQ_CUDA(cudaGetLastError(), "tq_select_pages: launch");
+        TQ_CUDA(launch(kern, grid, 1, kScoreThreads, query_smem(p.group, D) + static_cast<size_t>(p.room) * 8, st, p),
+                "tq_select_pages: launch");
         return TQ_OK;
     }
     // the selection itself does not depend on the type or the head size
@@ -263,19 +266,8 @@ tq_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaSt
     TQ_CUDA((prepare_kernel<kern>(kSortRoom * 4)), "tq_select_pages: cudaFuncSetAttribute");
     const unsigned tiles = (p.width + p.tile - 1) / p.tile;
     TQ_CUDA((prepare_kernel<score_kernel<T, D>>(score_smem<D>(8))), "tq_select_pages: cudaFuncSetAttribute");
-    score_kernel<T, D><<<grid * tiles, kScoreThreads, score_smem<D>(p.group), st>>>(p);
-    TQ_CUDA(cudaGetLastError(), "tq_select_pages: score launch");
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.room) * 4;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    TQ_CUDA(cudaLaunchKernelEx(&cfg, kern, p), "tq_select_pages: launch");
+    TQ_CUDA(launch(score_kernel<T, D>, grid * tiles, 1, kScoreThreads, score_smem<D>(p.group), st, p), "tq_select_pages: score launch");
+    TQ_CUDA(launch(kern, grid, 1, kSortThreads, static_cast<size_t>(p.room) * 4, st, p), "tq_select_pages: launch");
     return TQ_OK;
 }
 
@@ -382,20 +374,11 @@ tq_status launch_attend_pages(AttendPagesParams& p, int ctas, cudaStream_t st) {
     p.min_share = min_share<D>();
     constexpr auto kern = attend_pages_kernel<T, D>;
     TQ_CUDA((prepare_kernel<kern>(C::smem(8))), "tq_attend_pages: cudaFuncSetAttribute");
-    kern<<<ctas, C::kThreads, C::smem(p.group), st>>>(p);
-    TQ_CUDA(cudaGetLastError(), "tq_attend_pages: launch");
-    if (!p.direct && ctas > 1) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(p.rows_join ? p.rows_join : ctas - 1, (p.group + p.join_heads - 1) / p.join_heads);
-        cfg.blockDim = dim3(p.rows_join ? kJoinThreads : p.join_heads * D);   // going by shares: four slices
-        cfg.stream = st;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        TQ_CUDA(cudaLaunchKernelEx(&cfg, attend_pages_join_kernel<D>, p), "tq_attend_pages: join launch");
-    }
+    TQ_CUDA(launch(kern, ctas, 1, C::kThreads, C::smem(p.group), st, p), "tq_attend_pages: launch");
+    if (!p.direct && ctas > 1)
+        TQ_CUDA(launch(attend_pages_join_kernel<D>, p.rows_join ? p.rows_join : ctas - 1, (p.group + p.join_heads - 1) / p.join_heads,
+                       p.rows_join ? kJoinThreads : p.join_heads * D /* four slices */, 0, st, p),
+                "tq_attend_pages: join launch");
     return TQ_OK;
 }
 

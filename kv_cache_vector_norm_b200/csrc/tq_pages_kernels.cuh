@@ -14,6 +14,16 @@ namespace dev {
 
 constexpr int kPage = 16;
 
+// Every kernel here is launched as a programmatic dependent of what precedes it in the stream.  It begins by waiting
+// until all of that is complete and visible, and lets the kernel behind it be scheduled early (which waits in turn), so
+// that a step's launches do not each add their latency.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void release_stream() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void begin_dependent() {
+    wait_for_stream();
+    release_stream();
+}
+
 // ------------------------------------------------------------------------------------------ planning
 
 struct PlanParams {
@@ -80,8 +90,7 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
     __shared__ int s_len[NT], s_need[NT], s_from[NT], s_gone[NT], s_to[NT], s_req[NT];
     __shared__ int64_t s_row[NT];
     __shared__ int s_taken;
-    // the slot grid (a programmatic dependent) may be scheduled; it waits for this grid's completion
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_dependent();
     const int tid = threadIdx.x;
     const int cap = p.num_pages;
     int head = p.state[0], count = p.state[1];
@@ -185,7 +194,7 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
 __global__ void __launch_bounds__(kSlotTile) plan_slots_kernel(const PlanParams p) {
     __shared__ int64_t s_base[kSlotTile];
     __shared__ int s_ends[kSlotBatch];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_dependent();
     const int tid = threadIdx.x;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kSlotTile;
     const int n = static_cast<int>(p.max_tokens - t0 < kSlotTile ? p.max_tokens - t0 : kSlotTile);
@@ -279,6 +288,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, D == 256 && VALUES ? 2 : 3)
     constexpr int kBatch = 8;                            // rows in flight
     using Vec = typename Words<W>::type;
     const int lane = threadIdx.x & 31;
+    begin_dependent();
     const int64_t gw = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
     const int h = static_cast<int>(gw % p.heads);
     const int64_t t0 = gw / p.heads * p.tile;
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     uint4* slots = reinterpret_cast<uint4*>(qn + p.group * D) + threadIdx.x;   // [2][U][lo, hi][threads]
     __shared__ int32_t s_ids[kScoreTile];
     static_assert(kScoreTile == kScoreThreads, "a thread per page id");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_dependent();
     const int tiles = (p.width + p.tile - 1) / p.tile;
     const int row = blockIdx.x / tiles, b = row / p.heads, h = row - b * p.heads;
     const int64_t len = select_len(p, b);
@@ -551,8 +561,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// The `budget` best pages of one (sequence, kv head), by one CTA.  SCORED: score_kernel computes the keys, and this
-// grid is its programmatic dependent; else the CTA computes its row's keys first, several CTAs to an SM so that one
+// The `budget` best pages of one (sequence, kv head), by one CTA.  SCORED: score_kernel has computed the keys; else the
+// CTA computes its row's keys first, several CTAs to an SM so that one
 // row's selection runs under another's loads.
 //
 // The choice is a radix selection: the keys' range is cut into 256 bins, the bin that holds the budget-th largest
@@ -567,6 +577,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     __shared__ uint32_t s_hist[2][256];
     __shared__ uint32_t s_pick[3];
     __shared__ uint32_t s_warp[NW], s_warp2[NW];
+    begin_dependent();
     const int row = blockIdx.x;
     const int b = row / p.heads, h = row - b * p.heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -601,11 +612,6 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     uint32_t key[kHeld];
     int id[kHeld];
     if constexpr (SCORED) {
-        if (held) {                                      // before the scores are there
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) id[i] = j0 + i < j1 ? table[j0 + i] : -1;
-        }
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t* src = p.keys + static_cast<int64_t>(row) * p.width;
         if (held || nb > p.room) {
             keys = src;
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             key[i] = j0 + i < j1 ? (SCORED ? __ldcg(keys + j0 + i) : keys[j0 + i]) : 0u;
-            if (!SCORED) id[i] = j0 + i < j1 ? ids[j0 + i] : -1;
+            id[i] = j0 + i < j1 ? (SCORED ? table[j0 + i] : ids[j0 + i]) : -1;
         }
     }
     auto each = [&](auto f) {                            // f(page, its key, its id if it is held) for the thread's pages
@@ -781,11 +787,14 @@ struct PagesCfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kPageBytes = kPage * D * 2;                 // one page of keys (or values) of a kv head
-    static constexpr int kStages = (D == 64) ? 4 : 3;                // pages of keys and values in flight per warp
+    // Pages of keys and values in flight per warp, 96 to 128 KB per SM.  More only lengthens the queues at the memory,
+    // which SMs leave at different speeds while the shares are equal: 4, 3 and 3 pages at d = 64, 128 and 256 take
+    // 50.6, 89.6 and 94.4 us where 2 take 48.0, 85.4 and 92.1 (64 ragged sequences, 131072 tokens, 64 selected pages).
+    static constexpr int kStages = 2;
     static constexpr int kCtasPerSm = (D == 64) ? 3 : (D == 128) ? 2 : 1;
     static constexpr int kRing = kWarps * kStages * 2 * kPageBytes;
     // what a row costs besides its pages (its query, the joining of the warps' parts), in pages; a multiple of kWarps
-    static constexpr int kRowCost = D == 64 ? 8 : 4;
+    static constexpr int kRowCost = 8;
     static constexpr int kHeadStride = D + 4;                        // spreads the accumulator rows over the banks
     // floats per warp: m[8], l[8], O[G][D + 4].  What a group of fewer than 8 heads leaves free lets the join's CTAs
     // become resident before the last share is done.
@@ -918,6 +927,7 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
     const int gid = lane >> 2, tig = lane & 3;
     const int G = p.group;
 
+    wait_for_stream();
     // ---- this CTA's share
     int x0 = 0, x1, share = INT_MAX;
     PageCursor seg;                                      // the first page at or behind x0
@@ -973,7 +983,6 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         if (start >= static_cast<unsigned>(total)) {
             if (!p.rows_join && tid == 0) p.meta[blockIdx.x].row = -1;
             write_zeros();
-            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             return;
         }
         x0 = static_cast<int>(start);
@@ -1221,7 +1230,9 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         advance<C::kRowCost>(p, seg, seg.pages - seg.pg);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // only now: CTAs of the kernel behind this one that wait on an SM keep others of this grid's size from fitting when
+    // calls follow one another (64 ragged sequences at d = 64: 59.9 us with the release at the start, 50.6 us here)
+    release_stream();
 }
 
 // Joins the rows that lie in several shares.  out = sum O 2^(m - M) / sum l 2^(m - M).  With no more rows than shares
@@ -1236,7 +1247,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_pages_join_kernel(cons
     constexpr int kBatch = 8;                            // parts a thread reads at a time
     __shared__ float4 s_o[kJoinThreads];
     __shared__ float2 s_ml[kJoinThreads];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     const AttendPagesMeta m = p.meta[p.rows_join ? blockIdx.x : blockIdx.x + 1];
     if (m.row < 0) return;
     const int g0 = blockIdx.y * p.join_heads;
