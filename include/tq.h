@@ -514,14 +514,14 @@ typedef struct tq_select_args {
     const int32_t* seq_lens;   /* device [batch] (clamped to 0 .. max_blocks * 16) */
     int32_t* pages;            /* out, device [batch][num_kv_heads][budget]: head pages in ascending order, then -1 */
     int32_t* lens;             /* out, device [batch][num_kv_heads]: tokens of the listed pages */
-    void* workspace;           /* device scratch (4-byte aligned; may be NULL if none is needed): the scores of a call
+    void* workspace;           /* device scratch (16-byte aligned; may be NULL if none is needed): the scores of a call
                                   with few rows; needs no initialisation, overwritten by every call that uses it */
     size_t workspace_bytes;
 } tq_select_args;
 
 /*
  * tq_select_pages_workspace_bytes -- bytes of workspace tq_select_pages needs for these shapes on the current device:
- * 0, or 4 * batch * num_kv_heads * max_blocks when there are fewer (sequence, kv head) rows than SMs or rows are very
+ * 0, or about 4 * batch * num_kv_heads * max_blocks when there are fewer (sequence, kv head) rows than SMs or rows are very
  * long.  Only the shape fields are read.
  */
 tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* bytes);

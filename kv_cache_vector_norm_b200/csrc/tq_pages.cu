@@ -214,7 +214,7 @@ extern "C" tq_status tq_append_pages(const tq_append_args* a, void* stream) {
 namespace {
 
 constexpr int kSelSmem = 200 << 10;
-constexpr int kSortRoom = 32768;       // keys that select_kernel's SCORED form keeps in shared memory
+constexpr int kSortRoom = 24576;       // pages that select_kernel's SCORED form keeps in shared memory
 
 struct SelectPlan {
     bool scored;                       // the keys are computed by a grid of their own, through the workspace
@@ -235,19 +235,20 @@ tq_status plan_select(const char* fn, const tq_select_args* a, SelectPlan* plan)
             TQ_ERR_INVALID_ARG, "%s: budget=%d must hold keep_first=%d (>= 0) and keep_last=%d (>= 1) pages", fn, a->budget,
             a->keep_first, a->keep_last);
     const int64_t rows = static_cast<int64_t>(a->batch) * a->num_kv_heads;
-    const int width = a->max_blocks, even = (width + 1) & ~1;
+    const int width = a->max_blocks;
     // With fewer rows than SMs the scores take a grid over all pages; with many rows, or with few pages, a second
     // kernel costs more than it brings, unless a row's keys and page ids do not fit one CTA's shared memory.
-    const bool fits = query_smem(a->num_q_heads / a->num_kv_heads, a->head_dim) + static_cast<size_t>(even) * 8 <= kSelSmem;
+    const bool fits = key_stride(width) * 8 <= kSelSmem;
     plan->scored = !fits || (rows < device_sms() && width > kScoreTile);
-    plan->room = plan->scored ? (width < kSortRoom ? width : kSortRoom) : even;
+    plan->room = plan->scored && key_stride(width) > kSortRoom ? kSortRoom : static_cast<int>(key_stride(width));
     // two scoring CTAs to an SM with equal work, unless that leaves them little
     int64_t tile = (rows * width + 2 * device_sms() - 1) / (2 * device_sms());
     tile = (tile + 15) / 16 * 16;
     plan->tile = static_cast<int>(tile < 64 ? 64 : (tile > kScoreTile ? kScoreTile : tile));
     TQ_NEED(rows * ((width + plan->tile - 1) / plan->tile) < (1ll << 31), TQ_ERR_UNSUPPORTED,
             "%s: too many (sequence, kv head) rows for max_blocks=%d", fn, width);
-    plan->workspace_bytes = plan->scored ? static_cast<size_t>(rows) * width * 4 : 0;
+    plan->workspace_bytes =
+        plan->scored ? static_cast<size_t>(rows) * (static_cast<size_t>(key_stride(width)) + (width + plan->tile - 1) / plan->tile) * 4 : 0;
     return TQ_OK;
 }
 
@@ -257,17 +258,14 @@ tq_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaSt
     if (!scored) {
         constexpr auto kern = select_kernel<T, D, false>;
         TQ_CUDA((prepare_kernel<kern>(kSelSmem)), "tq_select_pages: cudaFuncSetAttribute");
-        TQ_CUDA(launch(kern, grid, 1, kScoreThreads, query_smem(p.group, D) + static_cast<size_t>(p.room) * 8, st, p),
-                "tq_select_pages: launch");
+        TQ_CUDA(launch(kern, grid, 1, kScoreThreads, static_cast<size_t>(p.room) * 8, st, p), "tq_select_pages: launch");
         return TQ_OK;
     }
-    // the selection itself does not depend on the type or the head size
-    constexpr auto kern = select_kernel<__half, 64, true>;
-    TQ_CUDA((prepare_kernel<kern>(kSortRoom * 4)), "tq_select_pages: cudaFuncSetAttribute");
+    constexpr auto kern = select_kernel<T, D, true>;
+    TQ_CUDA((prepare_kernel<kern>(kSortRoom * 8)), "tq_select_pages: cudaFuncSetAttribute");
     const unsigned tiles = (p.width + p.tile - 1) / p.tile;
-    TQ_CUDA((prepare_kernel<score_kernel<T, D>>(score_smem<D>(8))), "tq_select_pages: cudaFuncSetAttribute");
-    TQ_CUDA(launch(score_kernel<T, D>, grid * tiles, 1, kScoreThreads, score_smem<D>(p.group), st, p), "tq_select_pages: score launch");
-    TQ_CUDA(launch(kern, grid, 1, kSortThreads, static_cast<size_t>(p.room) * 4, st, p), "tq_select_pages: launch");
+    TQ_CUDA(launch(score_kernel<T, D>, grid * tiles, 1, kScoreThreads, 0, st, p), "tq_select_pages: score launch");
+    TQ_CUDA(launch(kern, grid, 1, kSortThreads, static_cast<size_t>(p.room) * 8, st, p), "tq_select_pages: launch");
     return TQ_OK;
 }
 
@@ -295,7 +293,7 @@ extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
             "%s: workspace of %zu bytes required (got %zu)", fn, plan.workspace_bytes, a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
     TQ_NEED(aligned(a->q, 16) && aligned(a->bounds, 16), TQ_ERR_INVALID_ARG, "%s: q and bounds must be 16-byte aligned", fn);
     TQ_NEED(a->q_stride % 8 == 0 && a->q_stride >= 0, TQ_ERR_INVALID_ARG, "%s: q_stride must be a non-negative multiple of 8", fn);
-    TQ_NEED(aligned(a->block_table, 4) && aligned(a->seq_lens, 4) && aligned(a->pages, 4) && aligned(a->lens, 4) && aligned(a->workspace, 4),
+    TQ_NEED(aligned(a->block_table, 4) && aligned(a->seq_lens, 4) && aligned(a->pages, 4) && aligned(a->lens, 4) && aligned(a->workspace, 16),
             TQ_ERR_INVALID_ARG, "%s: misaligned pointer in args", fn);
     SelectParams p;
     p.q = a->q;
@@ -314,9 +312,10 @@ extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
     p.keep_last = a->keep_last;
     p.tile = plan.tile;
     p.room = plan.room;
-    p.keys = static_cast<uint32_t*>(a->workspace);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t rows = static_cast<int64_t>(a->batch) * a->num_kv_heads;
+    p.keys = static_cast<uint32_t*>(a->workspace);
+    p.sizes = plan.scored ? reinterpret_cast<float*>(p.keys + rows * key_stride(p.width)) : nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_select, p, rows, plan.scored, st);
 }
 

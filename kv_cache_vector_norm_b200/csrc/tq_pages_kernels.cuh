@@ -391,105 +391,58 @@ struct SelectParams {
     int32_t* lens;                     // [B][H_kv]
     int heads, group, width, num_pages, budget, keep_first, keep_last;
     int tile;                          // pages a CTA of score_kernel scores
-    int room;                          // pages whose keys (and, unless SCORED, ids) select_kernel's shared memory holds
-    uint32_t* keys;                    // [B][H_kv][width]: keys of score_kernel (select_kernel's SCORED form)
+    int room;                          // pages whose keys and ids select_kernel's shared memory holds
+    uint32_t* keys;                    // [B][H_kv][key_stride]: keys of score_kernel (select_kernel's SCORED form)
+    float* sizes;                      // [B][H_kv][tiles]: see score_pages
 };
 
 constexpr int kScoreThreads = 256;     // threads that score pages together: a CTA of score_kernel, or of select_kernel
 constexpr int kScoreTile = 256;        // pages a CTA of score_kernel scores, at most
-constexpr int kSortThreads = 1024;     // threads of select_kernel's SCORED form
+constexpr int kSortThreads = 512;      // threads of select_kernel's SCORED form
 
-inline __host__ __device__ size_t query_smem(int group, int d) { return static_cast<size_t>(group) * d * 8; }
-
-// The query's heads of one kv head as max(q, 0) and min(q, 0) in shared memory, [G][2][d / 8][4]: lane l of a group
-// finds its channels 8 l .. 8 l + 7 in two 16-byte words without bank conflicts.
-template <typename T, int D>
-__device__ __forceinline__ void load_query(const SelectParams& p, int b, int h, float* qp, float* qn) {
-    const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<int64_t>(h) * p.group * D;
-    for (int i = threadIdx.x; i < p.group * D; i += kScoreThreads) {
-        const float x = static_cast<float>(q[i]);
-        const int g = i / D, c = i % D;
-        const int at = g * D + (c % 8 / 4) * (D / 2) + c / 8 * 4 + c % 4;
-        qp[at] = fmaxf(x, 0.f);
-        qn[at] = fminf(x, 0.f);
-    }
+// Keys of a row, in the workspace or in shared memory, are followed by others up to a multiple of kKeyGroup: a warp reads
+// four per lane at a time.
+constexpr int kKeyGroup = 128;
+inline __host__ __device__ int64_t key_stride(int width) {
+    return (static_cast<int64_t>(width) + kKeyGroup - 1) / kKeyGroup * kKeyGroup;
 }
 
-// One round of scoring: keys (order-preserving bits of the scores) of pages base .. base + U - 1 for each lane group of
-// d / 8 lanes, of the cnt pages from p0 on of a row of nb pages.  lo16, hi16: this lane's 8 channels of the bounds.
-//
-// The score of a page is max over the group's query heads of U_g = sum_c max(q_gc lo_c, q_gc hi_c), which is at least
-// q_g . k for every key in the page.  With lo <= hi the larger product is (q > 0 ? q hi : q lo), computed as two
-// fused multiply-adds of max(q, 0) with hi and min(q, 0) with lo: one of the products is a zero, and products of
-// 16-bit values are exact in fp32, so each step is a plain rounded addition.  The order of additions is part of the
-// operator (a lane's 8 channels as an even and an odd chain, then lanes i and i + half), so that the choice of pages
-// can be reproduced bit for bit; it also rules out the tensor cores, whose order is not defined.
-template <typename T, int D, int U>
-__device__ __forceinline__ void score_round(const SelectParams& p, const float4* qp4, const float4* qn4, const uint4 (&lo16)[U],
-                                            const uint4 (&hi16)[U], int nb, int p0, int cnt, int base, const int32_t* ids,
-                                            uint32_t* keys) {
-    constexpr int LP = D / 8;                            // lanes per page
-    static_assert(U == 2 || U == 4, "the reduction below spreads two or four pages over the lanes of a group");
-    constexpr int kHeads = U == 4 ? 2 : 1;               // heads in flight: one's products run under the other's shuffles
-    const int l = threadIdx.x % LP;
-    const bool upper = (l & (LP / 2)) != 0, odd = (l & (LP / 4)) != 0;
-    float2 lo[U][4], hi[U][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t aw[4] = {lo16[u].x, lo16[u].y, lo16[u].z, lo16[u].w};
-        const uint32_t cw[4] = {hi16[u].x, hi16[u].y, hi16[u].z, hi16[u].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lo[u][i] = Pair<T>::floats(aw[i]);
-            hi[u][i] = Pair<T>::floats(cw[i]);
-        }
-    }
-    float best = -INFINITY;
-#pragma unroll kHeads
-    for (int g = 0; g < p.group; ++g) {
-        const float4 p0v = qp4[g * (D / 4)], p1v = qp4[g * (D / 4) + LP];
-        const float4 n0v = qn4[g * (D / 4)], n1v = qn4[g * (D / 4) + LP];
-        const float2 pq[4] = {{p0v.x, p0v.y}, {p0v.z, p0v.w}, {p1v.x, p1v.y}, {p1v.z, p1v.w}};
-        const float2 nq[4] = {{n0v.x, n0v.y}, {n0v.z, n0v.w}, {n1v.x, n1v.y}, {n1v.z, n1v.w}};
-        float v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float2 acc = __fmul2_rn(pq[0], hi[u][0]);
-            acc = __ffma2_rn(nq[0], lo[u][0], acc);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                acc = __ffma2_rn(pq[i], hi[u][i], acc);
-                acc = __ffma2_rn(nq[i], lo[u][i], acc);
-            }
-            v[u] = acc.x + acc.y;
-        }
-        // lanes i and i + LP/2 add up, the upper half going on with one half of the pages and the lower with the
-        // other; then quarters
-        float s;
-        if constexpr (U == 4) {
-            const float k0 = upper ? v[2] : v[0], k1 = upper ? v[3] : v[1];
-            const float g0 = upper ? v[0] : v[2], g1 = upper ? v[1] : v[3];
-            const float w0 = k0 + __shfl_xor_sync(0xffffffffu, g0, LP / 2);
-            const float w1 = k1 + __shfl_xor_sync(0xffffffffu, g1, LP / 2);
-            s = (odd ? w1 : w0) + __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, LP / 4);
-        } else {
-            s = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], LP / 2);
-            s += __shfl_xor_sync(0xffffffffu, s, LP / 4);
-        }
-#pragma unroll
-        for (int o = LP / 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        // a sum that is not a number does not hide behind another head's
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(best) : "f"(s));
-    }
-    const int j = base + (U == 4 ? (upper ? 2 : 0) + (odd ? 1 : 0) : (upper ? 1 : 0));
-    if ((l & (LP / U - 1)) == 0 && j < cnt) {
-        const int at = p0 + j, id = ids[j];
-        uint32_t bits = __float_as_uint(best + 0.f);                 // -0 counts as 0
-        bits = (bits >> 31) ? ~bits : bits | 0x80000000u;
-        if (best != best || id < 0 || id >= p.num_pages) bits = 0u;
-        if (at < p.keep_first || at >= nb - p.keep_last) bits = 0xffffffffu;
-        keys[j] = bits;
-    }
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+
+__device__ __forceinline__ float max_nan(float a, float b) {         // not a number if one of the two is none
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Order-preserving bits of a score; -0 counts as 0, and what is not a number ranks below everything.
+__device__ __forceinline__ uint32_t score_key(float s) {
+    const uint32_t bits = __float_as_uint(s + 0.f);
+    return s != s ? 0u : ((bits >> 31) ? ~bits : bits | 0x80000000u);
+}
+__device__ __forceinline__ float key_score(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
 }
 
 __device__ __forceinline__ int64_t select_len(const SelectParams& p, int b) {
@@ -497,261 +450,461 @@ __device__ __forceinline__ int64_t select_len(const SelectParams& p, int b) {
     return len < 0 ? 0 : (len > most ? most : len);
 }
 
-// Keys of a call with few rows, where a CTA per row would leave most of the GPU idle: a CTA per row and kScoreTile
-// pages.  Four pages per lane group share each read of the query from shared memory.  With the registers that takes
-// there are 16 warps on an SM, too few to hide the loads, so each lane's next bounds are copied (cp.async) to a slot
-// that only it reads while it works on the ones before.
-template <int D>
-constexpr int score_smem(int group) { return static_cast<int>(query_smem(group, D)) + 2 * 4 * 2 * 16 * kScoreThreads; }
+// The score of a page is max over the group's query heads of U_g = sum_c max(q_gc lo_c, q_gc hi_c), which is at least
+// q_g . k for every key in the page.  With lo <= hi the larger product is (q > 0 ? q hi : q lo), so U_g is the product
+// of max(q, 0) with hi plus that of min(q, 0) with lo.  Products of 16-bit values are exact in fp32, and the order in
+// which they are added up is part of the operator, so that the choice of pages can be reproduced bit for bit.
+//
+// The tensor cores add in an order of their own, but nothing else is fast enough to keep up with the memory: on the
+// FMA pipe with that order 8192 pages x 8 kv heads x 8 query heads take 13 us, here 6.  So every score is first
+// computed on the tensor cores, together with its size sum |q| |bound| from the same operands, and the selection asks
+// for the scores in the defined order only where they could change its outcome (see select_kernel).
 
+// How far a score from the tensor cores may be from the one in the defined order, as a part of the largest size in the
+// row.  In that order a product takes part in at most 10 rounded additions: 10 2^-24.  The tensor cores make d / 8
+// steps in four chains of d / 32; a step adds 16 products to a sum, each cut off behind 24 bits of the largest: below
+// 17 d / 32 2^-23 of the chains' sizes, which add up to the row's.  Three more additions join the chains.
+template <int D>
+constexpr float kScoreError = (17.f * D / 32.f + 7.f) / 8388608.f;
+
+// Keys of the cnt pages from p0 on of a row of nb pages by the whole block, and the largest size among them (returned
+// to every thread of the warp that saw it).  ids: the pages' ids.  A warp takes 16 pages as the rows of its MMAs; head g
+// (or the last one) is column g.  The order of channels inside an MMA is free, so a lane's share of a row is 16-byte
+// words straight from memory: channels 32 c + 8 tig .. + 7 of rows gid and gid + 8 are the operands of two steps.
+template <typename T, int D>
+__device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h, int nb, int p0, int cnt, const int32_t* ids,
+                                             uint32_t* keys) {
+    using P = typename Pair<T>::type;
+    constexpr int NC = D / 32;                           // 16-byte words of a row per lane
+    constexpr int kBatch = NC < 4 ? NC : 4;              // of these, in flight at a time (for each of two rows, lo and hi)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    uint32_t pos[NC][4], neg[NC][4];                     // max(q, 0) and min(q, 0) of head gid
+    {
+        const T* q = static_cast<const T*>(p.q) + b * p.q_stride +
+                     (static_cast<int64_t>(h) * p.group + (gid < p.group ? gid : p.group - 1)) * D + 8 * tig;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(q + 32 * c));
+            pos[c][0] = max2<T>(w.x, 0u); pos[c][1] = max2<T>(w.y, 0u); pos[c][2] = max2<T>(w.z, 0u); pos[c][3] = max2<T>(w.w, 0u);
+            neg[c][0] = min2<T>(w.x, 0u); neg[c][1] = min2<T>(w.y, 0u); neg[c][2] = min2<T>(w.z, 0u); neg[c][3] = min2<T>(w.w, 0u);
+        }
+    }
+    const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + 8 * tig;
+    const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
+    float size = 0.f;
+    for (int j0 = warp * 16; j0 < cnt; j0 += kScoreThreads / 2) {
+        const T* src[2];
+        bool there[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int j = j0 + gid + 8 * r, id = j < cnt ? ids[j] : -1;
+            there[r] = id >= 0 && id < p.num_pages;
+            src[r] = bounds + (there[r] ? id : 0) * page_stride;
+        }
+        float s[4][4] = {}, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += kBatch) {
+            uint4 lo[kBatch][2], hi[kBatch][2];
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    lo[c][r] = hi[c][r] = make_uint4(0u, 0u, 0u, 0u);
+                    if (there[r]) {
+                        lo[c][r] = __ldg(reinterpret_cast<const uint4*>(src[r] + 32 * (c0 + c)));
+                        hi[c][r] = __ldg(reinterpret_cast<const uint4*>(src[r] + 32 * (c0 + c) + D));
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kBatch; ++c) {
+                const uint32_t(&qp)[4] = pos[c0 + c], (&qn)[4] = neg[c0 + c];
+                const uint4 &l0 = lo[c][0], &l1 = lo[c][1], &h0 = hi[c][0], &h1 = hi[c][1];
+                mma16816<T>(s[0], h0.x, h1.x, h0.y, h1.y, qp[0], qp[1]);
+                mma16816<T>(s[1], h0.z, h1.z, h0.w, h1.w, qp[2], qp[3]);
+                mma16816<T>(s[2], l0.x, l1.x, l0.y, l1.y, qn[0], qn[1]);
+                mma16816<T>(s[3], l0.z, l1.z, l0.w, l1.w, qn[2], qn[3]);
+                constexpr uint32_t kAbs = 0x7fff7fffu, kMinus = 0x80008000u;          // |hi| max(q, 0) - |lo| min(q, 0)
+                mma16816<T>(a, h0.x & kAbs, h1.x & kAbs, h0.y & kAbs, h1.y & kAbs, qp[0], qp[1]);
+                mma16816<T>(a, h0.z & kAbs, h1.z & kAbs, h0.w & kAbs, h1.w & kAbs, qp[2], qp[3]);
+                mma16816<T>(a, l0.x | kMinus, l1.x | kMinus, l0.y | kMinus, l1.y | kMinus, qn[0], qn[1]);
+                mma16816<T>(a, l0.z | kMinus, l1.z | kMinus, l0.w | kMinus, l1.w | kMinus, qn[2], qn[3]);
+            }
+        }
+        // rows gid and gid + 8: the maximum over the heads, columns 2 tig and 2 tig + 1 of this and the quad's lanes
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[0][e] = (s[0][e] + s[1][e]) + (s[2][e] + s[3][e]);
+        float best[2] = {max_nan(s[0][0], s[0][1]), max_nan(s[0][2], s[0][3])};
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            best[0] = max_nan(best[0], __shfl_xor_sync(0xffffffffu, best[0], o));
+            best[1] = max_nan(best[1], __shfl_xor_sync(0xffffffffu, best[1], o));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) size = a[e] > size && a[e] <= 3.402823466e38f ? a[e] : size;   // finite ones
+        const int j = j0 + gid + 8 * tig;
+        if (tig < 2 && j < cnt) {
+            uint32_t key = (tig ? there[1] : there[0]) ? score_key(tig ? best[1] : best[0]) : 0u;
+            const int at = p0 + j;
+            if (at < p.keep_first || at >= nb - p.keep_last) key = 0xffffffffu;
+            keys[j] = key;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
+    return size;
+}
+
+// The key of page `id` by its score in the defined order, by a whole warp: each 8 channels as an even and an odd chain,
+// the two added, then the upper half of the sums onto the lower.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t exact_key(const SelectParams& p, int b, int h, int id) {
+    constexpr int LP = D / 8;                            // lanes with channels; the others repeat theirs
+    const int l = (threadIdx.x & 31) % LP;
+    const T* page = static_cast<const T*>(p.bounds) + (static_cast<int64_t>(id) * p.heads + h) * 2 * D;
+    const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<int64_t>(h) * p.group * D + 8 * l;
+    const uint4 lw = __ldg(reinterpret_cast<const uint4*>(page + 8 * l)), hw = __ldg(reinterpret_cast<const uint4*>(page + D + 8 * l));
+    const uint32_t lo[4] = {lw.x, lw.y, lw.z, lw.w}, hi[4] = {hw.x, hw.y, hw.z, hw.w};
+    float best = -INFINITY;
+#pragma unroll 4
+    for (int g = 0; g < p.group; ++g) {
+        const uint4 qw = __ldg(reinterpret_cast<const uint4*>(q + g * D));
+        const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Pair<T>::floats(x[i]), a = Pair<T>::floats(lo[i]), c = Pair<T>::floats(hi[i]);
+            even = fmaf(fmaxf(f.x, 0.f), c.x, even);
+            even = fmaf(fminf(f.x, 0.f), a.x, even);
+            odd = fmaf(fmaxf(f.y, 0.f), c.y, odd);
+            odd = fmaf(fminf(f.y, 0.f), a.y, odd);
+        }
+        float s = even + odd;
+#pragma unroll
+        for (int o = LP / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        best = max_nan(best, s);
+    }
+    return score_key(best);
+}
+
+// Keys of a call with few rows, where a CTA per row would leave most of the GPU idle: a CTA per row and p.tile pages.
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectParams p) {
-    constexpr int U = 4, LP = D / 8, GW = 32 / LP;
-    constexpr int kRound = (kScoreThreads / 32) * GW * U;            // pages per round of the block
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* qp = reinterpret_cast<float*>(smem);
-    float* qn = qp + p.group * D;
-    uint4* slots = reinterpret_cast<uint4*>(qn + p.group * D) + threadIdx.x;   // [2][U][lo, hi][threads]
     __shared__ int32_t s_ids[kScoreTile];
+    __shared__ float s_size[kScoreThreads / 32];
     static_assert(kScoreTile == kScoreThreads, "a thread per page id");
     begin_dependent();
     const int tiles = (p.width + p.tile - 1) / p.tile;
-    const int row = blockIdx.x / tiles, b = row / p.heads, h = row - b * p.heads;
+    const int row = blockIdx.x / tiles, b = row / p.heads, h = row - b * p.heads, tile = blockIdx.x - row * tiles;
     const int64_t len = select_len(p, b);
-    const int p0 = (blockIdx.x - row * tiles) * p.tile;
-    load_query<T, D>(p, b, h, qp, qn);
-    if (p0 + threadIdx.x < p.width) s_ids[threadIdx.x] = p.table[static_cast<int64_t>(b) * p.width + p0 + threadIdx.x];
+    const int p0 = tile * p.tile;
+    if (threadIdx.x < p.tile && p0 + threadIdx.x < p.width)
+        s_ids[threadIdx.x] = p.table[static_cast<int64_t>(b) * p.width + p0 + threadIdx.x];
     const int nb = static_cast<int>((len + kPage - 1) / kPage);
     if (p0 >= nb || nb <= p.budget) return;
     const int cnt = nb - p0 < p.tile ? nb - p0 : p.tile;
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LP;
-    const float4* qp4 = reinterpret_cast<const float4*>(qp) + l;
-    const float4* qn4 = reinterpret_cast<const float4*>(qn) + l;
-    const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + l * 8;
-    const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
-    const int w0 = warp * GW * U;                        // the warp's first page of a round
-    auto fetch = [&](int round) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = round * kRound + w0 + lane / LP * U + u;
-            const int id = j < cnt ? s_ids[j] : -1;
-            if (id >= 0 && id < p.num_pages) {           // else the slot's old contents are scored and not used
-                const T* src = bounds + id * page_stride;
-                const uint32_t dst = smem_u32(slots + (round & 1) * U * 2 * kScoreThreads + u * 2 * kScoreThreads);
-                cp_async16(dst, src);
-                cp_async16(dst + 16 * kScoreThreads, src + D);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    fetch(0);
-    uint32_t* keys = p.keys + static_cast<int64_t>(row) * p.width + p0;
-    for (int round = 0; round * kRound + w0 < cnt; ++round) {
-        fetch(round + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        uint4 lo[U], hi[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            lo[u] = slots[((round & 1) * U + u) * 2 * kScoreThreads];
-            hi[u] = slots[((round & 1) * U + u) * 2 * kScoreThreads + kScoreThreads];
-        }
-        score_round<T, D, U>(p, qp4, qn4, lo, hi, nb, p0, cnt, round * kRound + w0 + lane / LP * U, s_ids, keys);
+    const float size = score_pages<T, D>(p, b, h, nb, p0, cnt, s_ids, p.keys + row * key_stride(p.width) + p0);
+    if ((threadIdx.x & 31) == 0) s_size[threadIdx.x >> 5] = size;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float m = 0.f;
+        for (int w = 0; w < kScoreThreads / 32; ++w) m = fmaxf(m, s_size[w]);
+        p.sizes[static_cast<int64_t>(row) * tiles + tile] = m;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // The `budget` best pages of one (sequence, kv head), by one CTA.  SCORED: score_kernel has computed the keys; else the
-// CTA computes its row's keys first, several CTAs to an SM so that one
-// row's selection runs under another's loads.
+// CTA computes its row's keys first, several CTAs to an SM so that one row's selection runs under another's loads.
 //
-// The choice is a radix selection: the keys' range is cut into 256 bins, the bin that holds the budget-th largest
-// key is found and cut again, until it goes in whole or holds one value, whose ties go to the lowest page index.  The
-// range starts at the smallest and largest score, not at the key's top bits, which all scores tend to share: two
-// passes usually do, and few keys fall into one bin at a time.  Pages kept in any case do not take part.
+// The choice is a radix selection: the keys' range is cut into 1024 bins and the bin that holds the budget-th largest
+// key is found.  The range starts at the smallest and largest score, not at the key's top bits, which all scores tend to
+// share.  Pages kept in any case do not take part.
+//
+// The keys are the tensor cores' scores.  With e the largest error these may have (kScoreError of the row's largest
+// size), a page more than 2 e above the bin is in by its score in the defined order too, and one more than 2 e below it
+// is out.  The others are put in a list, get their scores in the defined order and are ranked against each other, ties
+// by page index.  If the list cannot hold them all, these scores take the place of the keys, and the range is cut until
+// a bin goes in whole or holds one value.
+//
+// The work of one row is bound by the instructions of one SM, a few per key, so keys are read four at a time, what does
+// not compete has a key of its own (no tests of the page's index), and nothing is done per page that is left out.
 template <typename T, int D, bool SCORED>
-__global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : 4) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : (D == 64 ? 4 : D == 128 ? 3 : 2))
+    select_kernel(const SelectParams p) {
     constexpr int NT = SCORED ? kSortThreads : kScoreThreads;
     constexpr int NW = NT / 32;
+    constexpr int kList = 256, kBins = 1024, kBinBits = 10, kOwn = kBins / NT;    // bins of a thread
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint32_t s_hist[2][256];
+    __shared__ __align__(16) uint32_t s_hist[kBins];
     __shared__ uint32_t s_pick[3];
     __shared__ uint32_t s_warp[NW], s_warp2[NW];
+    __shared__ float s_size[NW];
+    __shared__ uint32_t s_key[kList];
+    __shared__ int s_page[kList];
+    __shared__ int s_listed[2];                          // entries of the list; those above the bin
     begin_dependent();
     const int row = blockIdx.x;
     const int b = row / p.heads, h = row - b * p.heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
     const int64_t len = select_len(p, b);
-    float* qp = reinterpret_cast<float*>(smem);
-    float* qn = qp + p.group * D;
-    uint32_t* room = reinterpret_cast<uint32_t*>(SCORED ? qp : qn + p.group * D);
-    int32_t* ids = reinterpret_cast<int32_t*>(room + p.room);
-    if constexpr (!SCORED) {                             // read while the length is on its way
-        load_query<T, D>(p, b, h, qp, qn);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+    int32_t* ids = reinterpret_cast<int32_t*>(keys + p.room);
+    // what does not depend on the length is read while that is on its way
+    if constexpr (SCORED) {
+        const uint32_t* src = p.keys + row * key_stride(p.width);
+#pragma unroll 4
+        for (int j = tid * 4; j < p.room; j += NT * 4)   // what lies behind the last key is overwritten below
+            *reinterpret_cast<uint4*>(keys + j) = __ldcg(reinterpret_cast<const uint4*>(src + j));
+    } else {
         for (int j = tid; j < p.width; j += NT) ids[j] = table[j];
     }
-    if (tid < 256) s_hist[0][tid] = s_hist[1][tid] = 0;
+    for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
+    if (tid < 2) s_listed[tid] = 0;
     const int nb = static_cast<int>((len + kPage - 1) / kPage);
     int32_t* out = p.pages + static_cast<int64_t>(row) * p.budget;
+    auto head_page = [&](int id) { return (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h; };
     if (tid == 0) p.lens[row] = static_cast<int>(nb <= p.budget ? len : len - static_cast<int64_t>(nb - p.budget) * kPage);
     if (nb <= p.budget) {                                // every page is kept
-        for (int j = tid; j < p.budget; j += NT) {
-            const int id = j < nb ? table[j] : -1;
-            out[j] = (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h;
-        }
+        for (int j = tid; j < p.budget; j += NT) out[j] = head_page(j < nb ? table[j] : -1);
         return;
     }
-    // Thread t looks after pages j0 .. j1 - 1.  Up to kHeld of them stay in registers; the keys of longer rows are read
-    // again in every pass (from shared memory, or from L2 if they do not fit there).
-    constexpr int kHeld = 8;
-    const int chunk = (nb + NT - 1) / NT;
-    const int j0 = tid * chunk < nb ? tid * chunk : nb, j1 = j0 + chunk < nb ? j0 + chunk : nb;
-    const bool held = chunk <= kHeld;
-    const uint32_t* keys = room;
-    uint32_t key[kHeld];
-    int id[kHeld];
+    float size = 0.f;
+    const int padded = static_cast<int>(key_stride(nb));
     if constexpr (SCORED) {
-        const uint32_t* src = p.keys + static_cast<int64_t>(row) * p.width;
-        if (held || nb > p.room) {
-            keys = src;
-        } else {
-#pragma unroll 4
-            for (int j = tid; j < nb; j += NT) room[j] = __ldcg(src + j);
-        }
+        __syncthreads();
+        // the passes over a very long sequence read the L2 cache
+        if (padded > p.room) keys = p.keys + row * key_stride(p.width);
+        const int tiles = (p.width + p.tile - 1) / p.tile, used = (nb + p.tile - 1) / p.tile;
+        for (int i = tid; i < used; i += NT) size = fmaxf(size, __ldcg(p.sizes + static_cast<int64_t>(row) * tiles + i));
+        for (int o = 16; o; o >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
     } else {
         __syncthreads();
-        constexpr int U = 2, LP = D / 8, GW = 32 / LP;
-        const int l = lane % LP;
-        const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + l * 8;
-        const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
-        for (int w0 = warp * GW * U; w0 < nb; w0 += NW * GW * U) {
-            const int base = w0 + lane / LP * U;
-            uint4 lo[U], hi[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int id = base + u < nb ? ids[base + u] : -1;
-                lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (id >= 0 && id < p.num_pages) {
-                    lo[u] = __ldg(reinterpret_cast<const uint4*>(bounds + id * page_stride));
-                    hi[u] = __ldg(reinterpret_cast<const uint4*>(bounds + id * page_stride + D));
-                }
-            }
-            score_round<T, D, U>(p, reinterpret_cast<const float4*>(qp) + l, reinterpret_cast<const float4*>(qn) + l, lo, hi, nb,
-                                 0, nb, base, ids, room);
-        }
+        size = score_pages<T, D>(p, b, h, nb, 0, nb, ids, keys);
     }
+    constexpr uint32_t kKept = 0xffffffffu;              // the key of pages that do not compete, and of none
+    if (nb + tid < padded) keys[nb + tid] = kKept;       // padded - nb < kKeyGroup <= NT
+    if (lane == 0) s_size[warp] = size;
     __syncthreads();
-    if (held) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            key[i] = j0 + i < j1 ? (SCORED ? __ldcg(keys + j0 + i) : keys[j0 + i]) : 0u;
-            id[i] = j0 + i < j1 ? (SCORED ? table[j0 + i] : ids[j0 + i]) : -1;
-        }
-    }
-    auto each = [&](auto f) {                            // f(page, its key, its id if it is held) for the thread's pages
-        if (held) {
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                if (j0 + i < j1) f(j0 + i, key[i], id[i]);
-        } else {
-            for (int j = j0; j < j1; ++j) f(j, keys[j], 0);
+    // Warp w looks after pages j0 .. j1 - 1, four to a lane.
+    const int chunk = (padded / kKeyGroup + NW - 1) / NW * kKeyGroup;
+    const int j0 = warp * chunk + lane * 4, j1 = (warp + 1) * chunk < padded ? (warp + 1) * chunk : padded;
+    auto each = [&](auto f) {                            // f(a key)
+#pragma unroll 1
+        for (int j = j0; j < j1; j += kKeyGroup) {
+            const uint4 k = *reinterpret_cast<const uint4*>(keys + j);
+            f(k.x); f(k.y); f(k.z); f(k.w);
         }
     };
-    // ---- the range of the keys that compete: pages c0 .. c1 - 1
-    const int c0 = p.keep_first, c1 = nb - p.keep_last < j1 ? nb - p.keep_last : j1;
-    uint32_t least = 0xffffffffu, most = 0u;
-    each([&](int j, uint32_t k, int) {
-        if (j >= c0 && j < c1) {
-            least = min(least, k);
-            most = max(most, k);
+    const uint32_t wanted = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);   // of those that compete
+    // smallest and largest of a value over the block
+    auto block_range = [&](uint32_t& least, uint32_t& most) {
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        __syncthreads();                                 // the sums before have been read
+        if (lane == 0) {
+            s_warp[warp] = least;
+            s_warp2[warp] = most;
         }
-    });
-    least = __reduce_min_sync(0xffffffffu, least);
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-        s_warp[warp] = least;
-        s_warp2[warp] = most;
-    }
-    __syncthreads();
-    least = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0xffffffffu);
-    most = __reduce_max_sync(0xffffffffu, lane < NW ? s_warp2[lane] : 0u);
-    // ---- the threshold: of the keys from `bound` to `bound` + 2^bits - 1, the `need` largest are in; all above are
-    uint32_t need = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);
-    int bits = 32 - __clz(static_cast<int>(most - least));
-    bool whole = need == 0;                              // everything from `bound` on is in
-    uint32_t bound = need == 0 ? 0xffffffffu : least;    // (need 0: nothing but the pages kept in any case)
-    for (int pass = 0; !whole; ++pass) {
-        const int shift = bits > 8 ? bits - 8 : 0;
-        const uint32_t width = bits == 32 ? 0xffffffffu : (1u << bits) - 1u;
-        uint32_t* hist = s_hist[pass & 1];
-        each([&](int j, uint32_t k, int) {
-            if (j >= c0 && j < c1 && k - bound <= width) atomicAdd(&hist[(k - bound) >> shift], 1u);
-        });
         __syncthreads();
-        // thread t takes bin 255 - t, so that an inclusive scan counts the keys from the largest bin down
-        uint32_t c = 0, incl = 0;
-        if (tid < 256) {
-            incl = c = hist[255 - tid];
-            s_hist[(pass & 1) ^ 1][tid] = 0;             // for the next pass
+        least = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0xffffffffu);
+        most = __reduce_max_sync(0xffffffffu, lane < NW ? s_warp2[lane] : 0u);
+    };
+    uint32_t from = 0xffffffffu, bound = 0xffffffffu, need = 0;      // in: keys from `from` on, and `need` equal to `bound`
+    if (wanted > 0) {
+        need = wanted;
+        float error = s_size[lane < NW ? lane : 0];
+        for (int o = 16; o; o >>= 1) error = fmaxf(error, __shfl_xor_sync(0xffffffffu, error, o));
+        error *= 2.f * kScoreError<D>;
+        int bits = 32;
+        bool exact = false;
+        for (bool again = true; again;) {
+            if (bits == 32) {
+                // the range of the keys that compete
+                uint32_t least = 0xffffffffu, most = 0u;
+                each([&](uint32_t k) {
+                    least = min(least, k);
+                    most = max(most, k + 1u);            // kKept: 0
+                });
+                block_range(least, most);
+                --most;
+                bound = least;
+                bits = 32 - __clz(static_cast<int>(most - least));
+            }
+            // count the keys from `bound` to `bound` + 2^bits - 1 in kBins bins and find the bin of the need-th largest
+            const int shift = bits > kBinBits ? bits - kBinBits : 0;
+            const uint32_t width = min(bits == 32 ? 0xffffffffu : (1u << bits) - 1u, kKept - 1u - bound);
+            each([&](uint32_t k) {
+                if (k - bound <= width) atomicAdd(&s_hist[(k - bound) >> shift], 1u);
+            });
+            __syncthreads();
+            // from the largest bin down: thread t takes kOwn bins from kBins - 1 - kOwn t on
+            const int top_bin = kBins - 1 - kOwn * tid;
+            uint32_t c[kOwn], incl = 0;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                c[i] = s_hist[top_bin - i];
+                s_hist[top_bin - i] = 0;                 // for the next pass
+                incl += c[i];
+            }
+            const uint32_t own = incl;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += t;
             }
             if (lane == 31) s_warp[warp] = incl;
-        }
-        __syncthreads();
-        if (tid < 256) {
+            __syncthreads();
+            uint32_t before = incl - own + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) incl += w < warp ? s_warp[w] : 0u;
-            if (incl >= need && incl - c < need) {       // one thread
-                s_pick[0] = 255u - tid;
-                s_pick[1] = incl - c;
-                s_pick[2] = incl;
+            for (int i = 0; i < kOwn; ++i) {
+                if (before < need && before + c[i] >= need) {        // one bin
+                    s_pick[0] = top_bin - i;
+                    s_pick[1] = before;
+                    s_pick[2] = before + c[i];
+                }
+                before += c[i];
             }
+            __syncthreads();
+            if (exact) {
+                bound += s_pick[0] << shift;
+                const bool whole = s_pick[2] == need;    // everything from `bound` on is in
+                need = whole ? 0u : need - s_pick[1];
+                bits = shift;
+                again = !whole && bits > 0;
+                from = whole ? bound : bound + 1;        // bound < 2^32 - 1: that key is of pages kept in any case
+                __syncthreads();                         // s_pick has been read
+                continue;
+            }
+            // the list: this bin's keys and those within the error of it
+            const uint32_t bottom = bound + (s_pick[0] << shift), top = bottom + ((1u << shift) - 1u);
+            const uint32_t low = min(bottom, score_key(__fsub_rd(key_score(bottom), error)));
+            const uint32_t high = max(top, score_key(__fadd_ru(key_score(top), error)));
+#pragma unroll 1
+            for (int j = j0; j < j1; j += kKeyGroup) {
+                const uint4 k4 = *reinterpret_cast<const uint4*>(keys + j);
+                const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (k[i] >= low && k[i] <= high) {
+                        const int at = atomicAdd(&s_listed[0], 1);
+                        if (k[i] > top) atomicAdd(&s_listed[1], 1);
+                        if (at < kList) {
+                            s_key[at] = k[i];
+                            s_page[at] = j + i;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            const int n = s_listed[0];
+            // entries of the list that are in
+            const int want = static_cast<int>(need) - (static_cast<int>(s_pick[1]) - s_listed[1]);
+            if (error == 0.f) {                          // without a size all scores are 0: nothing to compute
+                exact = true;
+                bits = 32;
+                continue;
+            }
+            if (n > kList) {
+#pragma unroll 1
+                for (int j = j0 - lane * 4 + lane; j < j1; j += 32) {
+                    const uint32_t k = keys[j];
+                    uint32_t now = k == kKept ? k : (k > high ? kKept - 1u : 0u);
+#pragma unroll 1
+                    for (unsigned rest = __ballot_sync(0xffffffffu, k != 0u && k >= low && k <= high); rest; rest &= rest - 1) {
+                        const int src = __ffs(rest) - 1;
+                        const uint32_t k2 = exact_key<T, D>(p, b, h, table[j - lane + src]);
+                        if (lane == src) now = k2;
+                    }
+                    keys[j] = now;
+                }
+                __syncthreads();
+                exact = true;
+                bits = 32;
+                continue;
+            }
+            bool in = want > 0;
+            const int page = tid < n ? s_page[tid] : 0;
+            if (want > 0 && want < n) {
+#pragma unroll 1
+                for (int x = warp; x < n; x += NW) {     // what is not a number (key 0) is so in any order
+                    const uint32_t k = s_key[x] ? exact_key<T, D>(p, b, h, table[s_page[x]]) : 0u;
+                    __syncwarp();
+                    if (lane == 0) s_key[x] = k;
+                }
+                __syncthreads();
+                if (tid < n) {
+                    const uint32_t mine = s_key[tid];
+                    int rank = 0;
+#pragma unroll 4
+                    for (int x = 0; x < n; ++x) rank += (s_key[x] > mine || (s_key[x] == mine && s_page[x] < page)) ? 1 : 0;
+                    in = rank < want;
+                }
+            }
+            if (tid < n) keys[page] = in ? kKept : 0u;
+            __syncthreads();
+            from = high + 1;                             // high < 2^32 - 1
+            need = 0;
+            again = false;
         }
-        __syncthreads();
-        bound += s_pick[0] << shift;
-        whole = s_pick[2] == need;
-        need -= s_pick[1];
-        bits = shift;
-        if (shift == 0) break;
     }
-    // ---- the list: keys from `from` on, and the first `need` of those equal to `bound`
-    const uint32_t from = whole ? bound : bound + 1;     // bound < 2^32 - 1: that key is of pages kept in any case
-    if (whole) need = 0;
+    // ---- the pages that are in, in ascending order
     uint32_t n_in = 0, n_tie = 0;
-    each([&](int, uint32_t k, int) {
+    each([&](uint32_t k) {
         n_in += k >= from ? 1u : 0u;
         n_tie += k < from && k == bound ? 1u : 0u;
     });
-    uint32_t in_before = n_in, ties_before = n_tie;      // in the threads before this one
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t a = __shfl_up_sync(0xffffffffu, in_before, o), t = __shfl_up_sync(0xffffffffu, ties_before, o);
-        if (lane >= o) {
-            in_before += a;
-            ties_before += t;
-        }
-    }
+    n_in = __reduce_add_sync(0xffffffffu, n_in);
+    n_tie = __reduce_add_sync(0xffffffffu, n_tie);
     __syncthreads();                                     // the sums before have been read
-    if (lane == 31) {
-        s_warp[warp] = in_before;
-        s_warp2[warp] = ties_before;
+    if (lane == 0) {
+        s_warp[warp] = n_in;
+        s_warp2[warp] = n_tie;
     }
     __syncthreads();
-    in_before += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u) - n_in;
-    ties_before += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u) - n_tie;
-    each([&](int j, uint32_t k, int page) {
-        const bool in = k >= from, tie = !in && k == bound;
-        if (in || (tie && ties_before < need)) {
-            const int e = held ? page : (SCORED ? table[j] : ids[j]);
-            out[in_before + (ties_before < need ? ties_before : need)] = (e < 0 || e >= p.num_pages) ? -1 : e * p.heads + h;
+    uint32_t in_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+    uint32_t ties_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u);
+#pragma unroll 1
+    for (int j = j0; j - lane * 4 < j1; j += kKeyGroup) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(keys + j);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        unsigned in = 0, tie = 0;                        // bit i: of the lane's i-th page
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            in |= k[i] >= from ? 1u << i : 0u;
+            tie |= k[i] < from && k[i] == bound ? 1u << i : 0u;
         }
-        in_before += in ? 1u : 0u;
-        ties_before += tie ? 1u : 0u;
-    });
+        uint32_t sum = __popc(in) + (__popc(tie) << 16);
+        const uint32_t own = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += t;
+        }
+        uint32_t i_at = in_before + ((sum - own) & 0xffffu), t_at = ties_before + ((sum - own) >> 16);
+#pragma unroll 1
+        for (unsigned rest = in | tie; rest; rest &= rest - 1) {
+            const int i = __ffs(rest) - 1;
+            const bool is_in = in >> i & 1u;
+            if (j + i < nb && (is_in || t_at < need)) {
+                const uint32_t at = i_at + (t_at < need ? t_at : need);
+                if (SCORED && at < static_cast<uint32_t>(p.room))
+                    ids[at] = j + i;                     // its id is looked up below
+                else
+                    out[at] = head_page(SCORED ? table[j + i] : ids[j + i]);
+            }
+            i_at += is_in ? 1u : 0u;
+            t_at += is_in ? 0u : 1u;
+        }
+        sum = __shfl_sync(0xffffffffu, sum, 31);
+        in_before += sum & 0xffffu;
+        ties_before += sum >> 16;
+    }
+    if constexpr (SCORED) {
+        __syncthreads();
+        for (int i = tid; i < p.budget && i < p.room; i += NT) out[i] = head_page(table[ids[i]]);
+    }
 }
 
 // -------------------------------------------------------------------- attention over uncompressed pages
@@ -802,28 +955,6 @@ struct PagesCfg {
     static constexpr int smem(int group) { return kRing + kWarps * comb(group) * 4; }
     static constexpr int kPart = 16 + 8 * D;                         // floats per partial: m[8], l[8], O[8][D]
 };
-
-template <typename T>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                 uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

@@ -677,8 +677,8 @@ def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
                  lens: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The `budget` pages of each (sequence, kv head) whose bounds allow the largest q . k (the first keep_first and
     last keep_last always): (pages int32 [B, H_kv, budget] of head pages, lens int32 [B, H_kv]), to be passed as
-    block_table and seq_lens to attend_pages or attend_decode.  workspace: scratch of 4 * B * H_kv * max_blocks bytes
-    (a call with few rows allocates it if it is not given)."""
+    block_table and seq_lens to attend_pages or attend_decode.  workspace: scratch of 5 * B * H_kv * max_blocks bytes
+    is always enough (a call with few rows allocates what it needs if it is not given)."""
     dtype, b, hq, d, q_stride = _q_rows(q)
     dev = q.device
     if bounds.dim() != 4:
