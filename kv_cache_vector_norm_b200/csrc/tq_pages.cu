@@ -203,8 +203,12 @@ extern "C" tq_status tq_append_pages(const tq_append_args* a, void* stream) {
     p.v_pool = a->v_pool;
     p.bounds = a->bounds;
     p.heads = a->num_kv_heads;
-    // a decode step's tokens lie in pages of their own: one warp each; a prefill's fill whole pages
-    p.tile = a->num_tokens * a->num_kv_heads <= 16384 ? 1 : 16;
+    // Whether tokens fill pages together or lie in pages of their own is not known here.  A warp per token suits the
+    // few tokens of a decode step (64 tokens in a page each, 8 heads of d = 128: 2.1 us; 16 tokens per warp: 14.2), 16
+    // tokens per warp a prefill (8192 in a row: 14.0 us; one per warp: 27.7); 4 in between (1024 tokens in a page each
+    // 6.2 us, in a row 4.7; one per warp 5.6 and 5.3, 16 per warp 13.6 and 3.3).
+    const int64_t rows = a->num_tokens * a->num_kv_heads;
+    p.tile = rows <= 2048 ? 1 : (rows <= 16384 ? 4 : 16);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_append, p, st);
 }

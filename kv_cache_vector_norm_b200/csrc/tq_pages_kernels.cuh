@@ -44,6 +44,7 @@ struct PlanParams {
 constexpr int kPlanThreads = 1024;      // requests a CTA of plan_kernel plans at a time, at most
 constexpr int kSlotTile = 256;         // tokens whose slots one CTA of plan_slots_kernel writes
 constexpr int kSlotBatch = 2048;       // row starts it keeps in shared memory
+constexpr int kCopies = 8;             // page ids a thread of plan_kernel moves at a time
 
 // Inclusive scan of two values over the block (every thread takes part); `total` receives the block's sums.
 template <int NT>
@@ -150,12 +151,26 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
             const int old = len_i < 0 ? ~len_i : (len_i + kPage - 1) / kPage;
             const int from = head + s_from[i];           // below 2 cap: from + j - head < count <= cap
             auto fresh = [&](int j) { return p.ring[from + j >= cap ? from + j - cap : from + j]; };
-#pragma unroll 4
-            for (int j = lane; j < need_i; j += per) row[old + j] = fresh(j);
+            // kCopies reads before the first write: nothing else tells the compiler that they do not overlap
+            for (int j0 = lane; j0 < need_i; j0 += per * kCopies) {
+                int id[kCopies];
+#pragma unroll
+                for (int u = 0; u < kCopies; ++u) id[u] = j0 + u * per < need_i ? fresh(j0 + u * per) : 0;
+#pragma unroll
+                for (int u = 0; u < kCopies; ++u)
+                    if (j0 + u * per < need_i) row[old + j0 + u * per] = id[u];
+            }
             const int64_t to_i = static_cast<int64_t>(count) + s_to[i];
-            for (int j = lane; j < gone_i && to_i + j < cap; j += per) {
-                const int at = static_cast<int>(to_i + j) - (cap - head);
-                p.ring[at < 0 ? at + cap : at] = row[j];
+            const int back = gone_i < cap - to_i ? gone_i : static_cast<int>(cap - to_i);
+            for (int j0 = lane; j0 < back; j0 += per * kCopies) {
+                int id[kCopies];
+#pragma unroll
+                for (int u = 0; u < kCopies; ++u) id[u] = j0 + u * per < back ? row[j0 + u * per] : 0;
+#pragma unroll
+                for (int u = 0; u < kCopies; ++u) {
+                    const int at = static_cast<int>(to_i + j0 + u * per) - (cap - head);
+                    if (j0 + u * per < back) p.ring[at < 0 ? at + cap : at] = id[u];
+                }
             }
             if (with_slots) {
                 // rows past max_tokens belong to requests that were refused
@@ -276,14 +291,14 @@ struct AppendParams {
     int heads, tile;                   // tokens whose page runs one warp looks after (1 .. 16)
 };
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 
 // One warp owns the page runs (consecutive input tokens of one kv head in one page) that start in its tile of
 // tokens, and follows the last one past the tile's end.  A run's rows are read once: stored to the pool and folded
 // into the page's channel bounds, which no other warp touches, so nothing is atomic and the result does not depend
 // on the order of warps.  A lane holds d / 32 channels of a row.  VALUES: there is a value pool.
 template <typename T, int D, bool VALUES>
-__global__ void __launch_bounds__(32 * kAppendWarps, D == 256 && VALUES ? 2 : 3) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, D == 256 && VALUES ? 4 : 6) append_kernel(const AppendParams p) {
     constexpr int W = D / 64;                            // words per lane and row
     constexpr int kBatch = 8;                            // rows in flight
     using Vec = typename Words<W>::type;
@@ -952,7 +967,10 @@ struct PagesCfg {
     // floats per warp: m[8], l[8], O[G][D + 4].  What a group of fewer than 8 heads leaves free lets the join's CTAs
     // become resident before the last share is done.
     static constexpr __host__ __device__ int comb(int group) { return 16 + group * kHeadStride; }
-    static constexpr int smem(int group) { return kRing + kWarps * comb(group) * 4; }
+    // d = 256 has no registers left for the query's fragments: each warp keeps its copy in shared memory
+    static constexpr bool kQueryInSmem = D == 256;
+    static constexpr int kQueryBytes = kQueryInSmem ? D / 16 * 32 * 8 : 0;
+    static constexpr int smem(int group) { return kRing + kWarps * (comb(group) * 4 + kQueryBytes); }
     static constexpr int kPart = 16 + 8 * D;                         // floats per partial: m[8], l[8], O[8][D]
 };
 
@@ -1218,14 +1236,21 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         const int row = seg.unit * p.mult + seg.m;
         const int row_begin = seg.x - seg.pg, row_end = row_begin + seg.pages;
         const int xe = row_end < x1 ? row_end : x1;
-        uint32_t qa[KS][2];
+        uint32_t qa[C::kQueryInSmem ? 1 : KS][2];
+        uint2* const qs = reinterpret_cast<uint2*>(comb + C::kWarps * C::comb(G)) + warp * (KS * 32) + lane;
         {
             const int b = row / p.heads, h = row - b * p.heads;
             const T* q = static_cast<const T*>(p.q) + b * p.q_stride + (static_cast<int64_t>(h) * G + gid) * D + 2 * tig;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                qa[ks][0] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks)) : 0u;
-                qa[ks][1] = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8)) : 0u;
+                const uint32_t a = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks)) : 0u;
+                const uint32_t c = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8)) : 0u;
+                if constexpr (C::kQueryInSmem) {
+                    qs[ks * 32] = make_uint2(a, c);      // read back by this lane only
+                } else {
+                    qa[ks][0] = a;
+                    qa[ks][1] = c;
+                }
             }
         }
         float o[KS][4];
@@ -1244,8 +1269,10 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
                 for (int ks = 0; ks < KS; ++ks) {
                     uint32_t f[4];
                     ldmatrix_x4(f, kb + ((mchunk ^ (2 * ks & 7)) << 4) + 128 * (ks / 4));
-                    mma16816<T>(sc[ks & 1][0], qa[ks][0], 0u, qa[ks][1], 0u, f[0], f[1]);
-                    mma16816<T>(sc[ks & 1][1], qa[ks][0], 0u, qa[ks][1], 0u, f[2], f[3]);
+                    uint2 a;
+                    if constexpr (C::kQueryInSmem) a = qs[ks * 32]; else a = make_uint2(qa[ks][0], qa[ks][1]);
+                    mma16816<T>(sc[ks & 1][0], a.x, 0u, a.y, 0u, f[0], f[1]);
+                    mma16816<T>(sc[ks & 1][1], a.x, 0u, a.y, 0u, f[2], f[3]);
                 }
                 // head gid, tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
                 float lg[4];
@@ -1295,8 +1322,11 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
                     if (valid < kPage) {                         // what lies behind the last token may be anything
                         f[0] &= vm0; f[1] &= vm0; f[2] &= vm1; f[3] &= vm1;
                     }
+                    // the page's part by itself: the tensor cores cut sums off where fp32 additions round
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816<T>(o[i], f[0], f[1], f[2], f[3], w0[t], w1[t]);
+                    for (int t = NT - 1; t >= 0; --t) mma16816<T>(part, f[0], f[1], f[2], f[3], w0[t], w1[t]);
+                    o[i][0] += part[0]; o[i][1] += part[1]; o[i][2] += part[2]; o[i][3] += part[3];
                 }
             }
             __syncwarp();                                        // every lane is done with the stage
