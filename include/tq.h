@@ -534,7 +534,8 @@ tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* by
  * lens counts the tokens of the listed pages (every page is full but a sequence's last, which is always listed last),
  * so pages and lens are a block table and lengths with one row per (sequence, kv head).  Read them with
  * tq_attend_pages (selected = 1), or with tq_attend_decode on the compressed pools as batch * num_kv_heads sequences
- * of one kv head: a head page is a page of a pool with one kv head.
+ * of one kv head: a head page is a page of a pool with one kv head.  A listed page whose table entry names no page is
+ * given as -1, which tq_attend_pages leaves out (tq_attend_decode needs entries that name pages).
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
  * result is the same on every run and for every shape of the call.  A score that is not a number ranks last.
  * Calls that overlap on the GPU must use distinct workspaces.

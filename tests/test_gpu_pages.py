@@ -57,7 +57,7 @@ def check_plan(new, lens, table, ring, state, heads, max_tokens, alias=False):
 
 @pytest.mark.parametrize("batch,heads,top,step,alias", [
     (1, 1, 40, 1, False), (1, 8, 5000, 5000, False), (7, 3, 100, 33, True), (64, 8, 600, 1, True), (64, 2, 300, 300, False),
-    (1024, 1, 60, 2, False), (1025, 2, 40, 20, True), (2500, 1, 30, 1, False)])
+    (1024, 1, 60, 2, False), (1025, 2, 40, 20, True), (2500, 1, 30, 1, False), (3, 2, 9000, 700, True)])
 @pytest.mark.parametrize("scarce", [False, True])
 def test_plan(batch, heads, top, step, alias, scarce):
     rng = np.random.default_rng(batch * 7 + heads + 1000 * scarce)
@@ -90,6 +90,17 @@ def test_plan_refuses_what_does_not_fit():
     # lengths that pass 32 bits together; an empty input
     check_plan([2 ** 30] * 3 + [1], [0, 0, 0, 1], np.array([[0], [1], [2], [3]]), np.arange(8), [0, 0], 1, 5)
     check_plan([0, -1], [0, 20], np.array([[-1, -1], [6, 2]]), np.full(8, -1), [7, 0], 4, 0)
+
+
+def test_plan_of_a_large_batch_with_few_tokens():
+    # more requests than the planning CTA has threads, and slots few enough that it writes them itself
+    rng = np.random.default_rng(2)
+    lens, new = rng.integers(0, 50, 1500), np.zeros(1500, dtype=np.int64)
+    new[[0, 3, 700, 1023, 1024, 1025, 1499]] = [40, 1, -1, 17, 33, -1, 2]
+    table, free = random_table(rng, lens, 6, 9000)
+    ring = np.full(9000, -1, dtype=np.int64)
+    ring[:len(free)] = free
+    check_plan(new, lens, table, ring, [0, len(free)], 3, 100)
 
 
 def test_plan_lengths_and_pages_that_are_wrong_are_contained():
@@ -198,7 +209,8 @@ def page_bounds(gen, num_pages, h, d, dtype):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("lens,h,g,budget,first,last", [
     ([0], 1, 1, 1, 0, 1), ([1, 16, 17], 2, 8, 2, 1, 1), ([100, 650, 0, 32, 641], 3, 4, 5, 1, 2), ([2049, 5000], 1, 7, 40, 4, 8),
-    ([9001], 2, 3, 100, 1, 1), ([40000, 39999], 1, 2, 64, 0, 1)])
+    ([9001], 2, 3, 100, 1, 1), ([40000, 39999], 1, 2, 64, 0, 1), ([16 * 24600 + 3], 1, 1, 700, 2, 1),
+    ([3000] * 80, 2, 1, 30, 1, 1), ([5000], 1, 5, 312, 1, 1)])
 def test_select(dtype, d, lens, h, g, budget, first, last):
     rng = np.random.default_rng(d + g)
     gen = torch.Generator(device=DEV).manual_seed(d + g)
@@ -217,6 +229,33 @@ def test_select_ties_go_to_the_lowest_index():
     for budget in (3, 100, 126, 127, 250, 499, 500, 501):
         check_select(q, bounds, np.arange(n)[None], [n * 16 - 5], budget, 1, 1)
     check_select(torch.zeros_like(q), -bounds.abs(), np.arange(n)[None], [n * 16], 77, 0, 1)           # zeros of either sign
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_select_scores_that_only_the_defined_order_tells_apart(dtype, d):
+    """Pages whose scores differ by less than the sums' own rounding: large terms, one channel a step apart.  A few of them
+    or more than a row's list of doubtful pages holds, with the threshold among them; the others lie above or below."""
+    gen = torch.Generator(device=DEV).manual_seed(d)
+    n = 700
+    dt = DTYPES[dtype]
+    q = torch.randn((1, 3, d), generator=gen, device=DEV).to(dt)
+    base = torch.sort(torch.randn((2, d), generator=gen, device=DEV), dim=0).values * 30
+    for near in (12, 200, 300, 650):
+        scale = torch.rand(n, generator=gen, device=DEV) * 0.5 + 1.2          # above, or the same below
+        scale[torch.arange(n, device=DEV) % 2 == 0] *= -1
+        bounds = torch.sort((base * scale[:, None, None]).to(dt).float(), dim=1).values
+        at = torch.randperm(n, generator=gen, device=DEV)[:near]
+        group = base.to(dt).float().repeat(near, 1, 1)
+        step = torch.randint(-3, 4, (near, 4), generator=gen, device=DEV) * torch.finfo(dt).eps
+        channel = torch.randint(0, d, (near, 4), generator=gen, device=DEV)
+        group[:, 1].scatter_(1, channel, group[:, 1].gather(1, channel) * (1 + step))
+        bounds[at] = torch.sort(group, dim=1).values
+        bounds = bounds.to(dt)[:, None].contiguous()
+        score = po.page_scores(q[0].float().cpu().numpy(), *(bounds[:, 0, i].float().cpu().numpy() for i in (0, 1)))
+        above = int((score > score[at.cpu().numpy()].max()).sum())
+        for budget in (above + 3, above + near // 2, above + near - 2):
+            check_select(q, bounds, np.arange(n)[None], [n * 16], min(max(budget, 2), n - 1), 1, 1)
 
 
 def test_select_bad_pages_and_numbers():
@@ -280,7 +319,7 @@ def forget_unused(kp, vp, table, lens):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("lens,h,g", [
     ([0], 1, 1), ([1], 1, 8), ([15, 16, 17], 2, 3), ([200, 0, 33, 0], 8, 4), ([64, 1, 0, 700, 129], 3, 5), ([3000], 2, 8),
-    ([0, 0, 1], 1, 2), ([1111, 5, 2048], 1, 7)])
+    ([0, 0, 1], 1, 2), ([1111, 5, 2048], 1, 7), ([0, 600, 0], 2, 1), ([530, 2], 150, 2)])
 def test_attend_pages(dtype, d, lens, h, g):
     rng = np.random.default_rng(d + h)
     gen = torch.Generator(device=DEV).manual_seed(d + g)
@@ -293,16 +332,20 @@ def test_attend_pages(dtype, d, lens, h, g):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-def test_attend_pages_many_short_sequences(dtype):
-    """More sequences than a CTA has threads, so the shares are found over several tiles of them; empty ones between."""
+@pytest.mark.parametrize("d,width,long", [(64, 4, 0), (64, 40, 0), (128, 40, 0), (256, 40, 0), (64, 400, 6000), (256, 200, 3100)])
+def test_attend_pages_many_sequences(dtype, d, width, long):
+    """More sequences than a CTA has threads and more rows than CTAs: empty ones between, all short, or a long one among
+    them that lies in many CTAs' shares.  Table rows of few pages take a CTA each."""
     rng = np.random.default_rng(1)
     gen = torch.Generator(device=DEV).manual_seed(2)
     lens = rng.integers(0, 60, 300)
     lens[::5], lens[128:140] = 0, 0
+    if long:
+        lens[77] = long
     num_pages = int(sum(-(-lens // 16)))
-    table, _ = random_table(rng, lens, 4, num_pages)
-    kp, vp = pools(gen, num_pages, 2, 64, DTYPES[dtype])
-    q = torch.randn((300, 4, 64), generator=gen, device=DEV).to(DTYPES[dtype])
+    table, _ = random_table(rng, lens, width, num_pages)
+    kp, vp = pools(gen, num_pages, 2, d, DTYPES[dtype])
+    q = torch.randn((300, 6, d), generator=gen, device=DEV).to(DTYPES[dtype])
     check_attend(q, kp, vp, table, lens)
 
 
