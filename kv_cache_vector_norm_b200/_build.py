@@ -1,4 +1,5 @@
-"""Build libtq.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libtq.so (the C-ABI library) in-tree with nvcc for sm_100a, and _bind.so (the compiled part of its Python
+binding) against the installed torch.
 
 Usage: ``python -m kv_cache_vector_norm_b200._build [--force] [--verbose]``.  The library is rebuilt
 when any source under csrc/ or include/ is newer than the existing .so.
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -29,9 +32,9 @@ def _sources():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
@@ -54,6 +57,24 @@ def _fresh(obj: str, src: str) -> bool:
 def nvcc() -> str:
     cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
+
+
+def _build_bind(verbose: bool) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           f"-I{sysconfig.get_paths()['include']}", "-I/usr/local/cuda/include", os.path.join(CSRC, "tq_bind.cpp"), "-o",
+           BIND + ".tmp", f"-L{PKG}", "-l:libtq.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if verbose or r.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout)
+    if r.returncode:
+        raise RuntimeError("compiling tq_bind.cpp failed")
+    os.replace(BIND + ".tmp", BIND)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -91,6 +112,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         sys.stderr.write(" ".join(link) + "\n" + r.stdout)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    _build_bind(verbose)
     if verbose:
         sys.stderr.write(f"built {LIB} in {time.time() - t0:.1f}s\n")
     return LIB

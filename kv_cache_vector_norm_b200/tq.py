@@ -1,8 +1,9 @@
 """Python binding of libtq (include/tq.h): argument marshalling only.
 
 Every computation runs in the library's CUDA kernels (or, for tq_make_rotation / tq_build_codebook, in
-its host C++).  PyTorch provides device memory and the current stream.  If libtq.so is missing this
-module raises at import time -- there is no fallback.
+its host C++).  PyTorch provides device memory and the current stream.  The paged-cache calls, whose kernels take a
+few microseconds in a decode step, are marshalled by compiled code (csrc/tq_bind.cpp).  If libtq.so or _bind.so is
+missing this module raises at import time -- there is no fallback.
 """
 from __future__ import annotations
 
@@ -164,6 +165,8 @@ def _load():
 
 
 LIB = _load()
+
+from . import _bind  # noqa: E402  (links libtq.so)
 
 
 class TQError(RuntimeError):
@@ -541,45 +544,6 @@ def attend_decode_noalloc(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv
 # ---------------------------------------------------------------------------------- the paged cache
 
 PAGE = 16                                               # tokens per page
-_PAGE_DTYPES = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
-
-# The raw handle of a device's current stream, without building a Stream object around it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _page_dtype(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    code = _PAGE_DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    return code
-
-
-def _need(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> int:
-    """Address of a contiguous tensor of this dtype, shape and device.  A decode step's calls take a few microseconds on
-    the GPU and pass up to ten tensors, so the checks are one expression."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}") from None
-    if t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
-    raise ValueError(f"{name} must be contiguous with shape {list(shape)}, got {list(t.shape)}")
-
-
-def _run_on(device: torch.device, name: str, fn, args, second=None):
-    """Make a call with `device` current; `second` is its second argument, by default that device's current stream."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        status = fn(args, _raw_stream(index) if second is None else second)
-    else:
-        with torch.cuda.device(device):
-            status = fn(args, _raw_stream(index) if second is None else second)
-    if status != TQ_OK:
-        raise TQError(name, status)
 
 
 @dataclass
@@ -603,40 +567,25 @@ def plan_pages(new_lens: torch.Tensor, seq_lens: torch.Tensor, block_table: torc
     free_state themselves."""
     if not isinstance(new_lens, torch.Tensor) or not new_lens.is_cuda:
         raise TypeError("new_lens must be a CUDA tensor")
-    dev, b = new_lens.device, new_lens.shape[0]
     if slots is None:
         if max_tokens is None:
             raise ValueError("plan_pages needs max_tokens or slots")
-        slots = torch.empty(max_tokens * num_kv_heads, dtype=torch.int64, device=dev)
+        slots = torch.empty(max_tokens * num_kv_heads, dtype=torch.int64, device=new_lens.device)
     elif max_tokens is None:
         max_tokens = slots.numel() // num_kv_heads
     if row_start is None:
-        row_start = torch.empty(b + 1, dtype=torch.int32, device=dev)
+        row_start = new_lens.new_empty(new_lens.numel() + 1, dtype=torch.int32)
     if start_pos is None:
-        start_pos = torch.empty(b, dtype=torch.int32, device=dev)
+        start_pos = torch.empty_like(new_lens, dtype=torch.int32)
     if seq_lens_out is None:
-        seq_lens_out = torch.empty(b, dtype=torch.int32, device=dev)
+        seq_lens_out = torch.empty_like(new_lens, dtype=torch.int32)
     if free_state_out is None:
-        free_state_out = torch.empty(2, dtype=torch.int32, device=dev)
-    i32, width, num_pages = torch.int32, block_table.shape[-1], free_pages.shape[0]
-    a = PlanArgs(b, num_kv_heads, width, num_pages, max_tokens,
-                 _need(new_lens, "new_lens", i32, (b,), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
-                 _need(block_table, "block_table", i32, (b, width), dev),
-                 _need(free_pages, "free_pages", i32, (num_pages,), dev), _need(free_state, "free_state", i32, (2,), dev),
-                 _need(slots, "slots", torch.int64, (max_tokens * num_kv_heads,), dev),
-                 _need(row_start, "row_start", i32, (b + 1,), dev), _need(start_pos, "start_pos", i32, (b,), dev),
-                 _need(seq_lens_out, "seq_lens_out", i32, (b,), dev),
-                 _need(free_state_out, "free_state_out", i32, (2,), dev))
-    _run_on(dev, "tq_plan_pages", LIB.tq_plan_pages, a)
+        free_state_out = new_lens.new_empty(2, dtype=torch.int32)
+    status = _bind.plan_pages(new_lens, seq_lens, block_table, free_pages, free_state, slots, row_start, start_pos,
+                              seq_lens_out, free_state_out, num_kv_heads, max_tokens)
+    if status:
+        raise TQError("tq_plan_pages", status)
     return PagePlan(slots, row_start, start_pos, seq_lens_out, free_state_out)
-
-
-def _rows(t: torch.Tensor, name: str, k: torch.Tensor, device):
-    """Address and strides of k, or of v beside it."""
-    token, head, unit = t.stride()
-    if unit != 1 or (t is not k and (t.shape != k.shape or t.dtype is not k.dtype or t.device != device)):
-        raise ValueError(f"{name} must be [N, H_kv, d] like k, with unit stride along d")
-    return t.data_ptr(), token, head
 
 
 def append_pages(k: torch.Tensor, v: torch.Tensor | None, slots: torch.Tensor, *, k_pool: torch.Tensor | None = None,
@@ -644,32 +593,9 @@ def append_pages(k: torch.Tensor, v: torch.Tensor | None, slots: torch.Tensor, *
     """Store k, v [N, H_kv, d] (fp16 or bf16; strided views of a fused projection are fine) at slots int64 [N * H_kv]
     of k_pool, v_pool [num_pages, H_kv, 16, d], and keep bounds [num_pages, H_kv, 2, d], the lowest and highest key of
     every page and channel.  Any of the three may be left out (bounds alone for a compressed cache)."""
-    dtype = _page_dtype(k, "k")
-    if k.dim() != 3:
-        raise ValueError("k must be [N, H_kv, d]")
-    n, h, d = k.shape
-    dev = k.device
-    some = k_pool if k_pool is not None else v_pool if v_pool is not None else bounds
-    pages = some.shape[0] if some is not None else 0
-    if v_pool is not None and v is None:
-        raise ValueError("v_pool needs v")
-    kp, k_tok, k_head = _rows(k, "k", k, dev)
-    vp, v_tok, v_head = _rows(v, "v", k, dev) if v is not None else (None, 0, 0)
-    kt, shape = k.dtype, (pages, h, PAGE, d)
-    a = AppendArgs(dtype, d, h, pages, n, kp, vp, k_tok, k_head, v_tok, v_head,
-                   _need(slots, "slots", torch.int64, (n * h,), dev),
-                   _need(k_pool, "k_pool", kt, shape, dev) if k_pool is not None else None,
-                   _need(v_pool, "v_pool", kt, shape, dev) if v_pool is not None else None,
-                   _need(bounds, "bounds", kt, (pages, h, 2, d), dev) if bounds is not None else None)
-    _run_on(dev, "tq_append_pages", LIB.tq_append_pages, a)
-
-
-def _q_rows(q: torch.Tensor):
-    """dtype code, sizes and batch stride of a query [B, H_q, d] whose sequences may lie apart."""
-    dtype, shape, strides = _page_dtype(q, "q"), q.shape, q.stride()
-    if len(shape) != 3 or strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]):
-        raise ValueError("q must be [B, H_q, d] with contiguous heads")
-    return dtype, *shape, strides[0]
+    status = _bind.append_pages(k, v, slots, k_pool, v_pool, bounds)
+    if status:
+        raise TQError("tq_append_pages", status)
 
 
 def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, *, budget: int,
@@ -677,68 +603,32 @@ def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
                  lens: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The `budget` pages of each (sequence, kv head) whose bounds allow the largest q . k (the first keep_first and
     last keep_last always): (pages int32 [B, H_kv, budget] of head pages, lens int32 [B, H_kv]), to be passed as
-    block_table and seq_lens to attend_pages or attend_decode.  workspace: scratch of 5 * B * H_kv * max_blocks bytes
-    is always enough (a call with few rows allocates what it needs if it is not given)."""
-    dtype, b, hq, d, q_stride = _q_rows(q)
-    dev = q.device
+    block_table and seq_lens to attend_pages or attend_decode.  workspace: scratch of 5 * B * H_kv * (max_blocks + 127)
+    bytes is always enough (a call with few rows allocates what it needs if it is not given)."""
     if bounds.dim() != 4:
         raise ValueError("bounds must be [num_pages, H_kv, 2, d]")
-    n, h = bounds.shape[:2]
     if pages is None:
-        pages = torch.empty((b, h, budget), dtype=torch.int32, device=dev)
+        pages = torch.empty((q.shape[0], bounds.shape[1], budget), dtype=torch.int32, device=q.device)
     if lens is None:
-        lens = torch.empty((b, h), dtype=torch.int32, device=dev)
-    i32, width = torch.int32, block_table.shape[-1]
-    a = SelectArgs(dtype, b, hq, h, d, width, n, budget, keep_first, keep_last, q.data_ptr(), q_stride,
-                   _need(bounds, "bounds", q.dtype, (n, h, 2, d), dev),
-                   _need(block_table, "block_table", i32, (b, width), dev), _need(seq_lens, "seq_lens", i32, (b,), dev),
-                   _need(pages, "pages", i32, (b, h, budget), dev), _need(lens, "lens", i32, (b, h), dev))
-    if workspace is None:
-        nb = ctypes.c_size_t()
-        _run_on(dev, "tq_select_pages_workspace_bytes", LIB.tq_select_pages_workspace_bytes, a, ctypes.byref(nb))
-        if nb.value:
-            workspace = torch.empty(nb.value, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise TypeError(f"workspace must be on {dev}")
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.nbytes
-    _run_on(dev, "tq_select_pages", LIB.tq_select_pages, a)
+        lens = torch.empty((q.shape[0], bounds.shape[1]), dtype=torch.int32, device=q.device)
+    status = _bind.select_pages(q, bounds, block_table, seq_lens, pages, lens, workspace, budget, keep_first, keep_last)
+    if status:
+        raise TQError("tq_select_pages", status)
     return pages, lens
 
 
-def _pool(t: torch.Tensor, name: str, dtype, device, shape: tuple):
-    """Address and page stride of a pool whose pages are contiguous but may lie apart (a half of a joint pool)."""
-    if t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name} must have the dtype and device of q")
-    page, head, row, unit = t.stride() if t.shape == shape else (0, 0, 0, 0)
-    if unit != 1 or row != shape[3] or head != PAGE * row:
-        raise ValueError(f"{name} must be {list(shape)}, each page contiguous; got {list(t.shape)}, strides {list(t.stride())}")
-    return t.data_ptr(), page
-
-
-def _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace) -> AttendPagesArgs:
-    dtype, b, hq, d, q_stride = _q_rows(q)
-    dev = q.device
-    n, h = k_pool.shape[:2]
-    shape, qt = (n, h, PAGE, d), q.dtype
-    kp, k_page = _pool(k_pool, "k_pool", qt, dev, shape)
-    vp, v_page = _pool(v_pool, "v_pool", qt, dev, shape)
-    rows = (b, h) if block_table.dim() == 3 else (b,)
-    width = block_table.shape[-1]
-    return AttendPagesArgs(dtype, b, hq, h, d, width, n, len(rows) - 1, scale, q.data_ptr(), q_stride, kp, vp, k_page,
-                           v_page, _need(block_table, "block_table", torch.int32, (*rows, width), dev),
-                           _need(seq_lens, "seq_lens", torch.int32, rows, dev),
-                           _need(out, "out", torch.float32, (b, hq, d), dev) if out is not None else None,
-                           workspace.data_ptr() if workspace is not None else None,
-                           workspace.nbytes if workspace is not None else 0)
-
-
 def attend_pages_workspace(q, k_pool, v_pool, block_table, seq_lens) -> torch.Tensor:
-    """A workspace of the size tq_attend_pages_workspace_bytes asks for."""
-    a = _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, 0.0, None, None)
+    """A workspace of the size tq_attend_pages_workspace_bytes asks for (at least 16 bytes)."""
+    a = AttendPagesArgs()
+    a.dtype = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}.get(q.dtype, -1)
+    a.batch, a.num_q_heads, a.head_dim = q.shape
+    a.num_pages, a.num_kv_heads = k_pool.shape[:2]
+    a.max_blocks, a.selected = block_table.shape[-1], int(block_table.dim() == 3)
     nb = ctypes.c_size_t()
-    _run_on(q.device, "tq_attend_pages_workspace_bytes", LIB.tq_attend_pages_workspace_bytes, a, ctypes.byref(nb))
-    return torch.empty(nb.value, dtype=torch.uint8, device=q.device)
+    with torch.cuda.device(q.device):
+        _check("tq_attend_pages_workspace_bytes",
+               LIB.tq_attend_pages_workspace_bytes(ctypes.byref(a), ctypes.byref(nb)))
+    return torch.empty(max(16, nb.value), dtype=torch.uint8, device=q.device)
 
 
 def attend_pages(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
@@ -746,15 +636,13 @@ def attend_pages(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, bl
                  workspace: torch.Tensor | None = None) -> torch.Tensor:
     """One decode step over uncompressed pages: q [B, H_q, d] (fp16 or bf16) against k_pool, v_pool [num_pages, H_kv,
     16, d], with block_table int32 [B, max_blocks] and seq_lens int32 [B], or the pages of a selection: block_table
-    [B, H_kv, n] and seq_lens [B, H_kv] (select_pages).  Returns out [B, H_q, d] f32."""
+    [B, H_kv, n] and seq_lens [B, H_kv] (select_pages).  Returns out [B, H_q, d] f32.  workspace:
+    attend_pages_workspace(...) or larger; allocated if it is not given."""
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = attend_pages_workspace(q, k_pool, v_pool, block_table, seq_lens)
-    elif workspace.device != q.device:
-        raise TypeError(f"workspace must be on {q.device}")
-    _run_on(q.device, "tq_attend_pages", LIB.tq_attend_pages,
-            _attend_pages_args(q, k_pool, v_pool, block_table, seq_lens, scale, out, workspace))
+    status = _bind.attend_pages(q, k_pool, v_pool, block_table, seq_lens, out, workspace, scale)
+    if status:
+        raise TQError("tq_attend_pages", status)
     return out
 
 

@@ -451,6 +451,57 @@ def test_pages_repeat_bitwise_and_on_two_streams():
         assert torch.equal(o, first)
 
 
+def test_binding_refusals():
+    """Wrong dtypes, shapes, layouts and devices are refused before anything is launched; so is what the library refuses."""
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    h, d, n = 2, 64, 9
+    kp, vp = pools(gen, n, h, d, torch.float16)
+    q = torch.zeros((3, 4, d), dtype=torch.float16, device=DEV)
+    tab, lens = i32(np.zeros((3, 40))), i32([1, 1, 1])
+    bounds = torch.zeros((n, h, 2, d), dtype=torch.float16, device=DEV)
+    slots = torch.zeros(10 * h, dtype=torch.int64, device=DEV)
+    k = torch.zeros((10, h, d), dtype=torch.float16, device=DEV)
+    state, ring = i32([0, 0]), i32(np.zeros(n))
+
+    def attend(q=q, kp=kp, vp=vp, tab=tab, lens=lens, **kw):
+        return tq.attend_pages(q, kp, vp, tab, lens, **kw)
+
+    def select(q=q, bounds=bounds, tab=tab, lens=lens, budget=4, **kw):
+        return tq.select_pages(q, bounds, tab, lens, budget=budget, **kw)
+
+    def append(k=k, v=k, slots=slots, kp=kp, vp=vp, bounds=bounds):
+        return tq.append_pages(k, v, slots, k_pool=kp, v_pool=vp, bounds=bounds)
+
+    def plan(new=lens, lens=lens, tab=tab, ring=ring, state=state, **kw):
+        return tq.plan_pages(new, lens, tab, ring, state, **{**dict(num_kv_heads=h, max_tokens=10), **kw})
+
+    attend(), select(), append(), plan()
+    bad = [
+        (TypeError, "float16", lambda: attend(q=q.float())), (TypeError, "CUDA", lambda: attend(q=q.cpu())),
+        (TypeError, "k_pool", lambda: attend(kp=kp.bfloat16())), (TypeError, "v_pool", lambda: attend(vp=vp.cpu())),
+        (ValueError, "v_pool", lambda: attend(vp=vp[:-1])), (ValueError, "k_pool", lambda: attend(kp=kp.transpose(1, 2))),
+        (TypeError, "block_table", lambda: attend(tab=tab.long())), (ValueError, "block_table", lambda: attend(tab=tab[:2])),
+        (ValueError, "block_table", lambda: attend(tab=tab.t().contiguous().t())), (ValueError, "seq_lens", lambda: attend(lens=lens[:2])),
+        (ValueError, "q must", lambda: attend(q=q.transpose(0, 1))), (ValueError, "out", lambda: attend(out=torch.zeros(3, 4, 2 * d, device=DEV))),
+        (TypeError, "workspace", lambda: attend(workspace=torch.zeros(1 << 20))),
+        (tq.TQError, "workspace of", lambda: attend(workspace=torch.zeros(16, device=DEV))),
+        (tq.TQError, "multiple", lambda: attend(q=q[:, :3].contiguous())), (TypeError, "must be real number", lambda: attend(scale="a")),
+        (TypeError, "bounds", lambda: select(bounds=bounds.bfloat16())), (ValueError, "bounds", lambda: select(bounds=bounds[:, :, :1].contiguous())),
+        (tq.TQError, "budget=1", lambda: select(budget=1)), (ValueError, "pages", lambda: select(pages=i32(np.zeros((3, h, 5))))),
+        (ValueError, "v must", lambda: append(v=k[:5])), (ValueError, "v_pool needs v", lambda: append(v=None)),
+        (ValueError, "slots", lambda: append(slots=slots[1:])), (TypeError, "slots", lambda: append(slots=slots.int())),
+        (ValueError, "bounds", lambda: append(bounds=bounds[1:])), (ValueError, "needs k_pool", lambda: append(kp=None, vp=None, bounds=None)),
+        (ValueError, "seq_lens", lambda: plan(lens=lens[:2])), (ValueError, "max_tokens or slots", lambda: plan(max_tokens=None)),
+        (ValueError, "slots", lambda: plan(slots=slots, max_tokens=3)), (TypeError, "free_pages", lambda: plan(ring=ring.cpu())),
+        (tq.TQError, "num_kv_heads=0", lambda: plan(num_kv_heads=0)), (tq.TQError, "max_tokens=-1", lambda: plan(slots=slots, max_tokens=-1))]
+    for kind, what, call in bad[:-1]:
+        with pytest.raises(kind, match=what):
+            call()
+    with pytest.raises((ValueError, tq.TQError)):
+        bad[-1][2]()
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------------------------------- used together
 
 @pytest.mark.parametrize("captured", [False, True])

@@ -117,9 +117,13 @@ def test_binding_checks_tensors():
     with pytest.raises(TypeError, match="k must"):
         tq.append_pages(torch.zeros(1, 1, 64, dtype=torch.float16), None, cpu)
     with pytest.raises(TypeError, match="q must"):
-        tq.select_pages(torch.zeros(1, 1, 64), cpu, cpu, cpu, budget=4)
+        tq.select_pages(torch.zeros(1, 1, 64), torch.zeros(1, 1, 2, 64), cpu, cpu, budget=4)
     with pytest.raises(TypeError, match="q must"):
         tq.attend_pages(torch.zeros(1, 1, 64, dtype=torch.float16), cpu, cpu, cpu, cpu, workspace=cpu)
+    with pytest.raises(TypeError, match="k must be a tensor, got list"):
+        tq.append_pages([1], None, cpu)
+    with pytest.raises(TypeError, match="expected 12 arguments"):
+        tq._bind.plan_pages(cpu)
 
 
 # ------------------------------------------------------------------------------ the plain implementations
