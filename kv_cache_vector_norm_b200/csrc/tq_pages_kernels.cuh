@@ -316,6 +316,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, D == 256 && VALUES ? 4 : 6)
     };
     // lane l looks at token t0 - 1 + l
     const int64_t slot = slot_of(t0 - 1 + lane);
+    if (p.tile == kPage) {                               // rows that are nearly sure to be read, while the slots come
+        constexpr int kLines = D / 64;                   // of 128 bytes, per row
+        for (int x = lane; x < kPage * kLines; x += 32) {
+            const int64_t t = t0 + x / kLines;
+            if (t < p.n) {
+                const int64_t at = x % kLines * 64 - lane * 2 * W;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(k + t * p.k_token + at));
+                if constexpr (VALUES) asm volatile("prefetch.global.L2 [%0];" ::"l"(v + t * p.v_token + at));
+            }
+        }
+    }
     const int64_t page = slot < 0 ? -1 : slot / kPage;
     const int64_t prev = __shfl_up_sync(0xffffffffu, page, 1);
     unsigned starts = __ballot_sync(0xffffffffu, page >= 0 && page != prev) & ((2u << p.tile) - 2u);
