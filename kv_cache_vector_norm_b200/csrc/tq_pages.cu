@@ -241,9 +241,11 @@ tq_status plan_select(const char* fn, const tq_select_args* a, SelectPlan* plan)
     const int64_t rows = static_cast<int64_t>(a->batch) * a->num_kv_heads;
     const int width = a->max_blocks;
     // With fewer rows than SMs the scores take a grid over all pages; with many rows, or with few pages, a second
-    // kernel costs more than it brings, unless a row's keys and page ids do not fit one CTA's shared memory.
+    // kernel costs more than it brings, unless a row's keys and page ids do not fit one CTA's shared memory.  Measured
+    // with two kernels and with one, d = 128: 8 rows of 300 pages 8.5 and 9.3 us, of 600 8.2 and 12.6, 128 rows of 300
+    // pages 12.8 and 10.4, of 600 18.2 and 22.8, 512 rows of 600 pages 51.8 and 49.5, of 200 33.0 and 26.2.
     const bool fits = key_stride(width) * 8 <= kSelSmem;
-    plan->scored = !fits || (rows < device_sms() && width > kScoreTile);
+    plan->scored = !fits || (rows < device_sms() && width > 384);
     plan->room = plan->scored && key_stride(width) > kSortRoom ? kSortRoom : static_cast<int>(key_stride(width));
     // two scoring CTAs to an SM with equal work, unless that leaves them little
     int64_t tile = (rows * width + 2 * device_sms() - 1) / (2 * device_sms());
