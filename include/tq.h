@@ -492,7 +492,8 @@ typedef struct tq_append_args {
  * pages' keys: bounds[page][h][0][c] and [1][c] are the minimum and maximum over the page's keys of channel c.  A
  * page whose first token (slot % 16 == 0) is among the rows starts anew; others extend the bounds they have.  For a
  * compressed cache only bounds is given and the rows go through tq_encode_k.
- * Rows not named by a slot are left as they were.  Tokens of one page and kv head must be consecutive input rows, as
+ * A key that is not a number counts in its page's bounds only if the channel has no other.  Rows not named by a slot are
+ * left as they were.  Tokens of one page and kv head must be consecutive input rows, as
  * tq_plan_pages lays them out (a page that appears in two places in one call gets undefined bounds); if a slot appears
  * twice, one of its rows is stored.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype).
@@ -537,7 +538,8 @@ tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* by
  * of one kv head: a head page is a page of a pool with one kv head.  A listed page whose table entry names no page is
  * given as -1, which tq_attend_pages leaves out (tq_attend_decode needs entries that name pages).
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
- * result is the same on every run and for every shape of the call.  A score that is not a number ranks last.
+ * result is the same on every run and for every shape of the call.  A score that is not a number ranks last.  (Not so
+ * where sum_c |q_c bounds_c| is past 2^126 or below 2^-100: which of the pages with such sums are kept is then undefined.)
  * Calls that overlap on the GPU must use distinct workspaces.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8, 2^39 pages or more in all rows).
  */
@@ -575,7 +577,9 @@ tq_status tq_attend_pages_workspace_bytes(const tq_attend_pages_args* args, size
  * tq_attend_pages -- attention of one new token per sequence over uncompressed pages: for each (b, hq), h = hq / G,
  *   p = softmax_t(scale * q . k_t),  out = sum_t p_t v_t   over tokens 0 .. seq_lens[b] - 1.
  * Scores, softmax and sums are fp32.  Rows of a page behind the sequence's last token may hold anything.  A sequence
- * of length 0, or whose table entries name no page, yields zeros.  The cache is read once, in equal shares per CTA
+ * of length 0, or whose table entries name no page, yields zeros, and so does one whose every score is -infinity.  A NaN
+ * in a token's key or in the query, or a score of +infinity, makes the head's output NaN, an infinity or NaN in a value
+ * its column of it.  The cache is read once, in equal shares per CTA
  * whatever the lengths; a second kernel (a programmatic dependent) joins the sequences that lie in several shares.
  * The same inputs give the same bits on every run.  Calls that overlap on the GPU must use distinct workspaces.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8).

@@ -373,6 +373,33 @@ def test_attend_pages_bad_pages_and_lengths():
     assert not got[2].any() and not got[3].any()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("width", [8, 120])
+def test_attend_pages_numbers_that_are_none(dtype, d, width):
+    """A NaN or an infinite score shows in the heads that read it, an infinite value in its column, and nowhere else; rows
+    whose scores are all -infinity give zeros.  Rows of one CTA, and rows joined from several."""
+    rng = np.random.default_rng(5)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    h, g, n = 2, 3, 16 * width - 5
+    table, _ = random_table(rng, [n] * 5, width, 5 * width)
+    kp, vp = pools(gen, 5 * width, h, d, DTYPES[dtype])
+    q = torch.randn((5, h * g, d), generator=gen, device=DEV).abs().add(0.1).to(DTYPES[dtype])
+    at = width - 2                                       # a page that is neither the first nor the last of its row
+    kp[int(table[0, at]), 1, 3, 7] = float("nan")
+    kp[int(table[1, at]), 0, 4, 0] = float("inf")
+    vp[int(table[2, at]), 1, 5, 9] = float("inf")
+    kp[torch.as_tensor(table[3]).long().to(DEV), 0, :, 2] = float("-inf")
+    q[4, 5, d - 1] = float("nan")
+    got = tq.attend_pages(q, kp, vp, torch.as_tensor(table, dtype=torch.int32, device=DEV),
+                          torch.full((5,), n, dtype=torch.int32, device=DEV)).cpu()
+    want = torch.zeros_like(got, dtype=torch.bool)
+    want[0, g:], want[1, :g], want[2, g:, 9], want[4, 5] = True, True, True, True
+    assert torch.equal(got.isfinite(), ~want)
+    assert got[0, g:].isnan().all() and got[1, :g].isnan().all() and got[4, 5].isnan().all()
+    assert not got[3, :g].any() and got[3, g:].all()
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_attend_pages_large_logits(d):
     """Logits far apart (running maximum, rescaling) and far from zero in every order of tokens."""
