@@ -142,8 +142,10 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     p.heads = a->num_kv_heads;
     p.max_tokens = a->max_tokens;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // a decode step's few slots are written by the planning CTA itself, a prefill's by a grid of their own
-    const bool one = a->max_tokens <= 1024;
+    // A decode step's few slots are written by the planning CTA itself, a prefill's by a grid of their own: with 8 heads
+    // 64 requests of one token take 3.2 us in one kernel and 6.8 in two, 512 take 6.7 and 7.8, 1024 take 10.3 and 7.5.
+    // Up to 256 requests a CTA of 256 threads scans faster than one of 1024 (64 requests: 3.2 us, 5.4).
+    const bool one = a->max_tokens * a->num_kv_heads <= 4096;
     TQ_CUDA(a->batch <= 256 && one ? launch(plan_kernel<256>, 1, 1, 256, 0, st, p, one)
                                    : launch(plan_kernel<kPlanThreads>, 1, 1, kPlanThreads, 0, st, p, one),
             "tq_plan_pages: launch");
@@ -333,7 +335,9 @@ namespace {
 template <int D>
 constexpr int min_share() { return PagesCfg<D>::kRowCost + PagesCfg<D>::kWarps; }
 
-// Table rows of at most this many pages are not split: a second launch takes longer than a CTA needs for them.
+// Table rows of at most this many pages are not split: a second launch takes longer than a CTA needs for them.  In one
+// kernel and in two, d = 128: 8 rows of 16 pages 5.2 and 7.5 us, of 32 7.5 and 7.7, of 48 9.6 and 7.7, of 64 11.9 and 7.7;
+// 512 rows of 32 26.3 and 29.5; d = 64, 512 rows of 64 30.9 and 28.1.
 constexpr int kDirectPages = 32;
 
 struct PagesPlan {
