@@ -141,17 +141,27 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     p.num_pages = a->num_pages;
     p.heads = a->num_kv_heads;
     p.max_tokens = a->max_tokens;
+    p.tile = kSlotTile;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // A decode step's few slots are written by the planning CTA itself, a prefill's by a grid of their own: with 8 heads
-    // 64 requests of one token take 3.2 us in one kernel and 6.8 in two, 512 take 6.7 and 7.8, 1024 take 10.3 and 7.5.
-    // Up to 256 requests a CTA of 256 threads scans faster than one of 1024 (64 requests: 3.2 us, 5.4).
-    const bool one = a->max_tokens * a->num_kv_heads <= 4096;
-    TQ_CUDA(a->batch <= 256 && one ? launch(plan_kernel<256>, 1, 1, 256, 0, st, p, one)
-                                   : launch(plan_kernel<kPlanThreads>, 1, 1, kPlanThreads, 0, st, p, one),
-            "tq_plan_pages: launch");
-    if (!one)
-        TQ_CUDA(launch(plan_slots_kernel, static_cast<unsigned>((a->max_tokens + kSlotTile - 1) / kSlotTile), 1, kSlotTile, 0, st, p),
-                "tq_plan_pages: slot launch");
+    // A decode step's few slots are written by the planning CTA itself, those of larger calls by a grid of their own: with
+    // 8 heads 64 requests of one token take 3.0 us in one kernel and 3.1 in two (and 2 us less on the host), 256 take 4.4
+    // and 3.4; past 256 requests, where that grid comes behind the plan, 512 take 6.4 and 7.8, 1024 take 10.3 and 7.2.  Up
+    // to 256 requests a CTA of 256 threads scans faster than one of 1024 (64 requests: 3.0 us, 5.4).
+    const bool few = a->batch <= kSlotTile;
+    const int64_t tiles = (a->max_tokens + kSlotTile - 1) / kSlotTile;
+    if (a->max_tokens * a->num_kv_heads <= (few ? 1024 : 4096)) {
+        TQ_CUDA(few ? launch(plan_kernel<kSlotTile, kPlanAll>, 1, 1, kSlotTile, 0, st, p)
+                    : launch(plan_kernel<kPlanThreads, kPlanAll>, 1, 1, kPlanThreads, 0, st, p),
+                "tq_plan_pages: launch");
+    } else if (few) {
+        const int64_t each = (tiles + device_sms() - 1) / device_sms();
+        p.tile = kSlotTile * static_cast<int>(each < kSlotTiles ? each : kSlotTiles);
+        TQ_CUDA(launch(plan_slots_ahead_kernel, static_cast<unsigned>((a->max_tokens + p.tile - 1) / p.tile), 1, kSlotTile, 0, st, p), "tq_plan_pages: slot launch");
+        TQ_CUDA(launch(plan_kernel<kSlotTile, kPlanBehindSlots>, 1, 1, kSlotTile, 0, st, p), "tq_plan_pages: launch");
+    } else {
+        TQ_CUDA(launch(plan_kernel<kPlanThreads, kPlanNoSlots>, 1, 1, kPlanThreads, 0, st, p), "tq_plan_pages: launch");
+        TQ_CUDA(launch(plan_slots_kernel, static_cast<unsigned>(tiles), 1, kSlotTile, 0, st, p), "tq_plan_pages: slot launch");
+    }
     return TQ_OK;
 }
 

@@ -39,10 +39,12 @@ struct PlanParams {
     int32_t* state_out;
     int batch, width, num_pages, heads;
     int64_t max_tokens;
+    int tile;                          // tokens of a CTA of plan_slots_ahead_kernel
 };
 
 constexpr int kPlanThreads = 1024;      // requests a CTA of plan_kernel plans at a time, at most
-constexpr int kSlotTile = 256;         // tokens whose slots one CTA of plan_slots_kernel writes
+constexpr int kSlotTile = 256;         // threads of the slots' kernels, and tokens they take at a time
+constexpr int kSlotTiles = 2;          // times that, at most, for a CTA of plan_slots_ahead_kernel
 constexpr int kSlotBatch = 2048;       // row starts it keeps in shared memory
 constexpr int kCopies = 8;             // page ids a thread of plan_kernel moves at a time
 
@@ -80,65 +82,105 @@ __device__ __forceinline__ int64_t page_slot(const PlanParams& p, int page, int6
     return (page < 0 || page >= p.num_pages) ? -1 : static_cast<int64_t>(page) * p.heads * kPage + pos % kPage;
 }
 
-// One CTA: lengths, admission, table rows and the free ring; with_slots: the slots too.  Admission is a prefix rule (a
-// request that needs pages gets them when the running sum of needs up to it is within the free count), so two scans
-// decide it for every request at once.  Pages are taken from the ring's start and given back at its end, so what this
-// call reads and what it writes never overlap, and a request's slots follow from its table row as it was and from its
-// part of the ring, without waiting for the table.
+// Admission is a prefix rule (a request that needs pages gets them when the running sum of needs up to it is within the
+// free count), so two scans decide it for every request at once.  Pages are taken from the ring's start and given back at
+// its end, so what a call reads of table and ring and what it writes there never overlap, and a request's slots follow
+// from its table row as it was and from its part of the ring, without waiting for the table.
+struct FreeRing {
+    int head, count;
+    __device__ explicit FreeRing(const PlanParams& p) : head(p.state[0]), count(p.state[1]) {
+        head = (head < 0 || head >= p.num_pages) ? 0 : head;
+        count = count < 0 ? 0 : (count > p.num_pages ? p.num_pages : count);
+    }
+    // the j-th page of those that are taken (j < count <= num_pages)
+    __device__ __forceinline__ int page(const PlanParams& p, int j) const {
+        return p.ring[head + j >= p.num_pages ? head + j - p.num_pages : head + j];
+    }
+};
+
+struct PlannedRequest {
+    bool active, finished, ok;
+    int64_t len, req, old_pages, end;                    // end: of its input rows
+    int64_t need, upto;                                  // pages it takes, and the needs up to and including it
+    int64_t gone, gone_end;                              // pages it gives back, and those up to and including it
+};
+
+struct PlanSums { int64_t rows = 0, gone = 0, need = 0; };           // of the requests before
+
+// Request b0 + threadIdx.x, by the whole block.
 template <int NT>
-__global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_slots) {
+__device__ __forceinline__ PlannedRequest plan_request(const PlanParams& p, int b0, int count, PlanSums& before,
+                                                       int64_t (*warp_sums)[2]) {
+    const int64_t most = static_cast<int64_t>(p.width) * kPage;
+    const int b = b0 + threadIdx.x;
+    PlannedRequest r;
+    r.active = b < p.batch;
+    const int want = r.active ? p.new_lens[b] : 0;
+    const int64_t len = r.active ? p.seq_lens[b] : 0;
+    r.finished = want < 0;
+    r.len = len < 0 ? 0 : (len > most ? most : len);
+    r.req = want > 0 ? want : 0;
+    r.old_pages = (r.len + kPage - 1) / kPage;
+    r.gone = r.finished ? r.old_pages : 0;
+    r.end = r.req;
+    r.gone_end = r.gone;
+    int64_t total[2];
+    block_scan2<NT>(r.end, r.gone_end, total, warp_sums);
+    r.end += before.rows;
+    r.gone_end += before.gone;
+    before.rows += total[0];
+    before.gone += total[1];
+    const bool fits = r.active && !r.finished && r.len + r.req <= most && r.end <= p.max_tokens;
+    r.need = fits ? (r.len + r.req + kPage - 1) / kPage - r.old_pages : 0;
+    int64_t unused = 0;
+    r.upto = r.need;
+    block_scan2<NT>(r.upto, unused, total, warp_sums);
+    r.upto += before.need;
+    before.need += total[0];
+    r.ok = fits && (r.need == 0 || r.upto <= count);
+    return r;
+}
+
+// What plan_kernel does: everything; all but the slots; or what plan_slots_ahead_kernel leaves to it.
+enum PlanPart { kPlanAll, kPlanNoSlots, kPlanBehindSlots };
+
+// One CTA: lengths, admission, the free ring, table rows and slots.
+template <int NT, PlanPart PART>
+__global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
     __shared__ int64_t s_warp[NT / 32][2];
     __shared__ int s_len[NT], s_need[NT], s_from[NT], s_gone[NT], s_to[NT], s_req[NT];
     __shared__ int64_t s_row[NT];
     __shared__ int s_taken;
-    begin_dependent();
+    // behind the slots' grid, which has waited for all before it, and whose writes are not read here
+    if constexpr (PART == kPlanBehindSlots) release_stream(); else begin_dependent();
     const int tid = threadIdx.x;
     const int cap = p.num_pages;
-    int head = p.state[0], count = p.state[1];
-    head = (head < 0 || head >= cap) ? 0 : head;
-    count = count < 0 ? 0 : (count > cap ? cap : count);
-    const int64_t most = static_cast<int64_t>(p.width) * kPage;
+    const FreeRing ring(p);
+    const int head = ring.head, count = ring.count;
     if (tid == 0) {
         s_taken = 0;
         p.row_start[0] = 0;
     }
-    int64_t rows_before = 0, gone_before = 0, need_before = 0, total[2];
+    PlanSums sums;
+    int len_out = 0;
     for (int b0 = 0; b0 < p.batch; b0 += NT) {
         const int b = b0 + tid;
-        const bool active = b < p.batch;
-        const int want = active ? p.new_lens[b] : 0;
-        int64_t len = active ? p.seq_lens[b] : 0;
-        len = len < 0 ? 0 : (len > most ? most : len);
-        const int64_t req = want > 0 ? want : 0;
-        const int64_t old_pages = (len + kPage - 1) / kPage;
-        const int64_t gone = want < 0 ? old_pages : 0;
-        int64_t end = req, gone_end = gone;
-        block_scan2<NT>(end, gone_end, total, s_warp);
-        end += rows_before;
-        gone_end += gone_before;
-        rows_before += total[0];
-        gone_before += total[1];
-        const bool fits = active && want >= 0 && len + req <= most && end <= p.max_tokens;
-        const int64_t need = fits ? (len + req + kPage - 1) / kPage - old_pages : 0;
-        int64_t upto = need, unused = 0;
-        block_scan2<NT>(upto, unused, total, s_warp);
-        upto += need_before;
-        need_before += total[0];
-        const bool ok = fits && (need == 0 || upto <= count);
-        if (ok && need > 0) atomicMax(&s_taken, static_cast<int>(upto));
-        if (active) {
-            p.row_start[b + 1] = end > INT_MAX ? INT_MAX : static_cast<int>(end);
-            p.start_pos[b] = ok ? static_cast<int>(len) : -1;
-            p.seq_lens_out[b] = want < 0 ? 0 : static_cast<int>(len + (ok ? req : 0));
+        const PlannedRequest r = plan_request<NT>(p, b0, count, sums, s_warp);
+        if (r.ok && r.need > 0) atomicMax(&s_taken, static_cast<int>(r.upto));
+        len_out = r.finished ? 0 : static_cast<int>(r.len + (r.ok ? r.req : 0));
+        if (r.active) {
+            p.row_start[b + 1] = r.end > INT_MAX ? INT_MAX : static_cast<int>(r.end);
+            p.start_pos[b] = r.ok ? static_cast<int>(r.len) : -1;
+            if constexpr (PART != kPlanBehindSlots) p.seq_lens_out[b] = len_out;
         }
-        const int64_t to = gone_end - gone;
-        s_len[tid] = ok ? static_cast<int>(len) : ~static_cast<int>(old_pages);     // refused: the pages it has
-        s_need[tid] = ok ? static_cast<int>(need) : 0;
-        s_from[tid] = ok ? static_cast<int>(upto - need) : 0;
-        s_gone[tid] = static_cast<int>(gone);
+        const int64_t to = r.gone_end - r.gone;
+        s_len[tid] = r.ok ? static_cast<int>(r.len) : ~static_cast<int>(r.old_pages);     // refused: the pages it has
+        s_need[tid] = r.ok ? static_cast<int>(r.need) : 0;
+        s_from[tid] = r.ok ? static_cast<int>(r.upto - r.need) : 0;
+        s_gone[tid] = static_cast<int>(r.gone);
         s_to[tid] = to > cap ? cap : static_cast<int>(to);
-        s_req[tid] = static_cast<int>(req);
-        s_row[tid] = end - req;
+        s_req[tid] = static_cast<int>(r.req);
+        s_row[tid] = r.end - r.req;
         __syncthreads();
         // table rows, ring and slots: the block's threads in equal groups, a request per group
         const int n = p.batch - b0 < NT ? p.batch - b0 : NT;
@@ -147,18 +189,18 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
         const int lane = tid & (per - 1);
         for (int i = tid / per; i < n; i += NT / per) {
             int32_t* row = p.table + static_cast<int64_t>(b0 + i) * p.width;
-            const int need_i = s_need[i], gone_i = s_gone[i], len_i = s_len[i];
+            const int need_i = s_need[i], gone_i = s_gone[i], len_i = s_len[i], from = s_from[i];
             const int old = len_i < 0 ? ~len_i : (len_i + kPage - 1) / kPage;
-            const int from = head + s_from[i];           // below 2 cap: from + j - head < count <= cap
-            auto fresh = [&](int j) { return p.ring[from + j >= cap ? from + j - cap : from + j]; };
             // kCopies reads before the first write: nothing else tells the compiler that they do not overlap
-            for (int j0 = lane; j0 < need_i; j0 += per * kCopies) {
-                int id[kCopies];
+            if constexpr (PART != kPlanBehindSlots) {
+                for (int j0 = lane; j0 < need_i; j0 += per * kCopies) {
+                    int id[kCopies];
 #pragma unroll
-                for (int u = 0; u < kCopies; ++u) id[u] = j0 + u * per < need_i ? fresh(j0 + u * per) : 0;
+                    for (int u = 0; u < kCopies; ++u) id[u] = j0 + u * per < need_i ? ring.page(p, from + j0 + u * per) : 0;
 #pragma unroll
-                for (int u = 0; u < kCopies; ++u)
-                    if (j0 + u * per < need_i) row[old + j0 + u * per] = id[u];
+                    for (int u = 0; u < kCopies; ++u)
+                        if (j0 + u * per < need_i) row[old + j0 + u * per] = id[u];
+                }
             }
             const int64_t to_i = static_cast<int64_t>(count) + s_to[i];
             const int back = gone_i < cap - to_i ? gone_i : static_cast<int>(cap - to_i);
@@ -172,7 +214,7 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
                     if (j0 + u * per < back) p.ring[at < 0 ? at + cap : at] = id[u];
                 }
             }
-            if (with_slots) {
+            if constexpr (PART == kPlanAll) {
                 // rows past max_tokens belong to requests that were refused
                 const int64_t left = p.max_tokens - s_row[i];
                 const int rows = static_cast<int>(left < 0 ? 0 : (s_req[i] < left ? s_req[i] : left));
@@ -183,7 +225,7 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
                     if (len_i >= 0) {
                         const int64_t pos = static_cast<int64_t>(len_i) + t;
                         const int pg = static_cast<int>(pos / kPage);
-                        slot = page_slot(p, pg < old ? row[pg] : fresh(pg - old), pos);
+                        slot = page_slot(p, pg < old ? row[pg] : ring.page(p, from + pg - old), pos);
                     }
                     dst[e] = slot < 0 ? -1 : slot + (e - t * p.heads) * kPage;
                 }
@@ -191,21 +233,97 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p, bool with_
         }
         __syncthreads();
     }
-    if (with_slots) {                                    // input rows behind the last request's
-        for (int64_t e = rows_before * p.heads + tid; e < p.max_tokens * p.heads; e += NT) p.slots[e] = -1;
+    if constexpr (PART == kPlanAll) {                    // input rows behind the last request's
+        for (int64_t e = sums.rows * p.heads + tid; e < p.max_tokens * p.heads; e += NT) p.slots[e] = -1;
+    }
+    if constexpr (PART == kPlanBehindSlots) {            // the slots' grid reads what these may overwrite
+        wait_for_stream();
+        if (tid < p.batch) p.seq_lens_out[tid] = len_out;            // batch <= NT
     }
     if (tid == 0) {
         const int taken = s_taken;
         const int64_t room = cap - count;
-        const int back = static_cast<int>(gone_before < room ? gone_before : room);
+        const int back = static_cast<int>(sums.gone < room ? sums.gone : room);
         const int next = head + taken;
         p.state_out[0] = next >= cap ? next - cap : next;
         p.state_out[1] = count - taken + back;
     }
 }
 
-// Slots of larger calls, after plan_kernel: one CTA per kSlotTile input rows, one search per token for its request
-// (in shared memory up to kSlotBatch requests), then the tokens' H_kv slots with coalesced stores.
+// The slots of a CTA's n tokens from the first slot of each, with coalesced stores.
+__device__ __forceinline__ void write_slots(const PlanParams& p, int64_t t0, int n, const int64_t* base) {
+    int64_t* dst = p.slots + t0 * p.heads;
+    const int t_step = kSlotTile / p.heads, h_step = kSlotTile - t_step * p.heads;
+    int t = threadIdx.x / p.heads, h = threadIdx.x - t * p.heads;
+    for (int i = threadIdx.x; i < n * p.heads; i += kSlotTile) {
+        dst[i] = base[t] < 0 ? -1 : base[t] + h * kPage;
+        t += t_step;
+        h += h_step;
+        if (h >= p.heads) {
+            h -= p.heads;
+            ++t;
+        }
+    }
+}
+
+// The first of n requests whose rows end after `token`.
+__device__ __forceinline__ int request_of(const int* ends, int n, int64_t token) {
+    int lo = 0;
+    while (lo < n) {
+        const int mid = (lo + n) >> 1;
+        if (ends[mid] <= token) lo = mid + 1; else n = mid;
+    }
+    return lo;
+}
+
+// Slots and table rows of larger calls of up to kSlotTile requests, before plan_kernel and beside it: a CTA per p.tile
+// input rows that plans the whole batch for itself, which costs less than waiting for another kernel's plan (8 heads, 64
+// requests of 64 tokens: 3.3 us, 8.1 with the slots behind the plan; 116736 tokens: 5.6 and 10.3, with one or four times
+// kSlotTile rows to a CTA 6.7 and 5.9).  A new page is entered in its table row with its first token.
+__global__ void __launch_bounds__(kSlotTile) plan_slots_ahead_kernel(const PlanParams p) {
+    __shared__ int64_t s_warp[kSlotTile / 32][2];
+    __shared__ int64_t s_base[kSlotTile * kSlotTiles];
+    __shared__ int s_ends[kSlotTile], s_len[kSlotTile], s_from[kSlotTile];
+    begin_dependent();
+    const int tid = threadIdx.x;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tile;
+    const int n = static_cast<int>(p.max_tokens - t0 < p.tile ? p.max_tokens - t0 : p.tile);
+    const FreeRing ring(p);
+    PlanSums sums;
+    const PlannedRequest r = plan_request<kSlotTile>(p, 0, ring.count, sums, s_warp);
+    s_ends[tid] = r.end > INT_MAX ? INT_MAX : static_cast<int>(r.end);
+    s_len[tid] = r.ok ? static_cast<int>(r.len) : -1;
+    s_from[tid] = r.ok ? static_cast<int>(r.upto - r.need) : 0;
+    __syncthreads();
+    int at[kSlotTiles], id[kSlotTiles];           // all reads before the first write
+    int64_t pos[kSlotTiles];
+#pragma unroll
+    for (int u = 0; u < kSlotTiles; ++u) {
+        const int64_t token = t0 + u * kSlotTile + tid;
+        id[u] = -1;
+        pos[u] = 1;
+        if (u * kSlotTile + tid < n) {
+            const int b = request_of(s_ends, p.batch, token);
+            const int len = b < p.batch ? s_len[b] : -1;
+            if (len >= 0) {
+                pos[u] = len + (token - (b ? s_ends[b - 1] : 0));
+                const int pg = static_cast<int>(pos[u] / kPage), old = (len + kPage - 1) / kPage;
+                at[u] = b;
+                id[u] = pg < old ? p.table[static_cast<int64_t>(b) * p.width + pg] : ring.page(p, s_from[b] + pg - old);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kSlotTiles; ++u) {
+        if (pos[u] % kPage == 0) p.table[static_cast<int64_t>(at[u]) * p.width + pos[u] / kPage] = id[u];   // a new page
+        s_base[u * kSlotTile + tid] = page_slot(p, id[u], pos[u]);
+    }
+    __syncthreads();
+    write_slots(p, t0, n, s_base);
+}
+
+// The same for larger batches, after plan_kernel and by its results: one search per token for its request (in shared
+// memory up to kSlotBatch requests).
 __global__ void __launch_bounds__(kSlotTile) plan_slots_kernel(const PlanParams p) {
     __shared__ int64_t s_base[kSlotTile];
     __shared__ int s_ends[kSlotBatch];
@@ -222,24 +340,16 @@ __global__ void __launch_bounds__(kSlotTile) plan_slots_kernel(const PlanParams 
     int64_t base = -1;
     if (tid < n) {
         const int64_t token = t0 + tid;
-        int lo = 0, hi = p.batch;                        // the first request whose rows end after `token`
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (ends[mid] <= token) lo = mid + 1; else hi = mid;
-        }
-        if (lo < p.batch) {
-            const int start = p.start_pos[lo];
-            const int64_t pos = start + (token - (lo ? ends[lo - 1] : 0));
-            if (start >= 0) base = page_slot(p, p.table[static_cast<int64_t>(lo) * p.width + pos / kPage], pos);
+        const int b = request_of(ends, p.batch, token);
+        if (b < p.batch) {
+            const int start = p.start_pos[b];
+            const int64_t pos = start + (token - (b ? ends[b - 1] : 0));
+            if (start >= 0) base = page_slot(p, p.table[static_cast<int64_t>(b) * p.width + pos / kPage], pos);
         }
     }
     s_base[tid] = base;
     __syncthreads();
-    int64_t* dst = p.slots + t0 * p.heads;
-    for (int i = tid; i < n * p.heads; i += kSlotTile) {
-        const int t = i / p.heads, h = i - t * p.heads;
-        dst[i] = s_base[t] < 0 ? -1 : s_base[t] + h * kPage;
-    }
+    write_slots(p, t0, n, s_base);
 }
 
 // ------------------------------------------------------------------------------- appending to pages

@@ -78,6 +78,25 @@ def test_plan(batch, heads, top, step, alias, scarce):
     assert len(set(stored.tolist())) == len(stored)
 
 
+@pytest.mark.parametrize("batch,heads,step", [(200, 8, 600), (256, 1, 500), (257, 1, 500), (256, 3, 6), (255, 4, 1), (256, 4, 1), (1, 5, 99999)])
+@pytest.mark.parametrize("scarce", [False, True])
+def test_plan_writes_over_its_inputs(batch, heads, step, scarce):
+    """Lengths and ring state updated in place, at the batch and slot counts where the launches change."""
+    rng = np.random.default_rng(batch + heads + 1000 * scarce)
+    lens, new = rng.integers(0, 99, batch), rng.integers(min(step, 2), step + 1, batch)
+    lens[::7], new[batch // 2:batch // 2 + 2] = 0, [-1, 0][:len(new[batch // 2:batch // 2 + 2])]
+    if batch == 1:
+        new[0] = step
+    width = -(-(99 + step) // 16)
+    num_pages = batch * width + 1
+    table, free = random_table(rng, lens, width, num_pages)
+    need = int(sum(-(-(l + max(n, 0)) // 16) - -(-l // 16) for l, n in zip(lens, new)))
+    count, head = need * 3 // 4 if scarce else need, num_pages - 3
+    ring = np.full(num_pages, -7, dtype=np.int64)
+    ring[(head + np.arange(count)) % num_pages] = free[:count]
+    check_plan(new, lens, table, ring, [head, count], heads, int(np.maximum(new, 0).sum()), True)
+
+
 def test_plan_refuses_what_does_not_fit():
     # request 1 passes its table row, 3 the input rows (and so do all behind it), 5 finishes all the same
     lens, new = [10, 60, 0, 5, 20, 33], [6, 10, 16, 40, 1, -1]
