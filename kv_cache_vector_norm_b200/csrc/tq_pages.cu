@@ -150,16 +150,16 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     const bool few = a->batch <= kSlotTile;
     const int64_t tiles = (a->max_tokens + kSlotTile - 1) / kSlotTile;
     if (a->max_tokens * a->num_kv_heads <= (few ? 1024 : 4096)) {
-        TQ_CUDA(few ? launch(plan_kernel<kSlotTile, kPlanAll>, 1, 1, kSlotTile, 0, st, p)
-                    : launch(plan_kernel<kPlanThreads, kPlanAll>, 1, 1, kPlanThreads, 0, st, p),
+        TQ_CUDA(few ? launch(plan_kernel<kSlotTile, true>, 1, 1, kSlotTile, 0, st, p)
+                    : launch(plan_kernel<kPlanThreads, true>, 1, 1, kPlanThreads, 0, st, p),
                 "tq_plan_pages: launch");
     } else if (few) {
         const int64_t each = (tiles + device_sms() - 1) / device_sms();
         p.tile = kSlotTile * static_cast<int>(each < kSlotTiles ? each : kSlotTiles);
         TQ_CUDA(launch(plan_slots_ahead_kernel, static_cast<unsigned>((a->max_tokens + p.tile - 1) / p.tile), 1, kSlotTile, 0, st, p), "tq_plan_pages: slot launch");
-        TQ_CUDA(launch(plan_kernel<kSlotTile, kPlanBehindSlots>, 1, 1, kSlotTile, 0, st, p), "tq_plan_pages: launch");
+        TQ_CUDA(launch(plan_beside_kernel, 1, 1, kSlotTile, 0, st, p), "tq_plan_pages: launch");
     } else {
-        TQ_CUDA(launch(plan_kernel<kPlanThreads, kPlanNoSlots>, 1, 1, kPlanThreads, 0, st, p), "tq_plan_pages: launch");
+        TQ_CUDA(launch(plan_kernel<kPlanThreads, false>, 1, 1, kPlanThreads, 0, st, p), "tq_plan_pages: launch");
         TQ_CUDA(launch(plan_slots_kernel, static_cast<unsigned>(tiles), 1, kSlotTile, 0, st, p), "tq_plan_pages: slot launch");
     }
     return TQ_OK;

@@ -141,18 +141,37 @@ __device__ __forceinline__ PlannedRequest plan_request(const PlanParams& p, int 
     return r;
 }
 
-// What plan_kernel does: everything; all but the slots; or what plan_slots_ahead_kernel leaves to it.
-enum PlanPart { kPlanAll, kPlanNoSlots, kPlanBehindSlots };
+// The first of n requests whose rows (or pages) end after `token`.
+__device__ __forceinline__ int request_of(const int* ends, int n, int64_t token) {
+    int lo = 0;
+    while (lo < n) {
+        const int mid = (lo + n) >> 1;
+        if (ends[mid] <= token) lo = mid + 1; else n = mid;
+    }
+    return lo;
+}
 
-// One CTA: lengths, admission, the free ring, table rows and slots.
-template <int NT, PlanPart PART>
+__device__ __forceinline__ int plan_len(const PlannedRequest& r) {   // after the step
+    return r.finished ? 0 : static_cast<int>(r.len + (r.ok ? r.req : 0));
+}
+__device__ __forceinline__ void write_rows(const PlanParams& p, int b, const PlannedRequest& r) {
+    p.row_start[b + 1] = r.end > INT_MAX ? INT_MAX : static_cast<int>(r.end);
+    p.start_pos[b] = r.ok ? static_cast<int>(r.len) : -1;
+}
+__device__ __forceinline__ void write_state(const PlanParams& p, const FreeRing& ring, int taken, int64_t gone) {
+    const int room = p.num_pages - ring.count, next = ring.head + taken;
+    p.state_out[0] = next >= p.num_pages ? next - p.num_pages : next;
+    p.state_out[1] = ring.count - taken + static_cast<int>(gone < room ? gone : room);
+}
+
+// One CTA: lengths, admission, the free ring and table rows; SLOTS: the slots too.
+template <int NT, bool SLOTS>
 __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
     __shared__ int64_t s_warp[NT / 32][2];
     __shared__ int s_len[NT], s_need[NT], s_from[NT], s_gone[NT], s_to[NT], s_req[NT];
     __shared__ int64_t s_row[NT];
     __shared__ int s_taken;
-    // behind the slots' grid, which has waited for all before it, and whose writes are not read here
-    if constexpr (PART == kPlanBehindSlots) release_stream(); else begin_dependent();
+    begin_dependent();
     const int tid = threadIdx.x;
     const int cap = p.num_pages;
     const FreeRing ring(p);
@@ -162,16 +181,12 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
         p.row_start[0] = 0;
     }
     PlanSums sums;
-    int len_out = 0;
     for (int b0 = 0; b0 < p.batch; b0 += NT) {
-        const int b = b0 + tid;
         const PlannedRequest r = plan_request<NT>(p, b0, count, sums, s_warp);
         if (r.ok && r.need > 0) atomicMax(&s_taken, static_cast<int>(r.upto));
-        len_out = r.finished ? 0 : static_cast<int>(r.len + (r.ok ? r.req : 0));
         if (r.active) {
-            p.row_start[b + 1] = r.end > INT_MAX ? INT_MAX : static_cast<int>(r.end);
-            p.start_pos[b] = r.ok ? static_cast<int>(r.len) : -1;
-            if constexpr (PART != kPlanBehindSlots) p.seq_lens_out[b] = len_out;
+            write_rows(p, b0 + tid, r);
+            p.seq_lens_out[b0 + tid] = plan_len(r);
         }
         const int64_t to = r.gone_end - r.gone;
         s_len[tid] = r.ok ? static_cast<int>(r.len) : ~static_cast<int>(r.old_pages);     // refused: the pages it has
@@ -192,15 +207,13 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
             const int need_i = s_need[i], gone_i = s_gone[i], len_i = s_len[i], from = s_from[i];
             const int old = len_i < 0 ? ~len_i : (len_i + kPage - 1) / kPage;
             // kCopies reads before the first write: nothing else tells the compiler that they do not overlap
-            if constexpr (PART != kPlanBehindSlots) {
-                for (int j0 = lane; j0 < need_i; j0 += per * kCopies) {
-                    int id[kCopies];
+            for (int j0 = lane; j0 < need_i; j0 += per * kCopies) {
+                int id[kCopies];
 #pragma unroll
-                    for (int u = 0; u < kCopies; ++u) id[u] = j0 + u * per < need_i ? ring.page(p, from + j0 + u * per) : 0;
+                for (int u = 0; u < kCopies; ++u) id[u] = j0 + u * per < need_i ? ring.page(p, from + j0 + u * per) : 0;
 #pragma unroll
-                    for (int u = 0; u < kCopies; ++u)
-                        if (j0 + u * per < need_i) row[old + j0 + u * per] = id[u];
-                }
+                for (int u = 0; u < kCopies; ++u)
+                    if (j0 + u * per < need_i) row[old + j0 + u * per] = id[u];
             }
             const int64_t to_i = static_cast<int64_t>(count) + s_to[i];
             const int back = gone_i < cap - to_i ? gone_i : static_cast<int>(cap - to_i);
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
                     if (j0 + u * per < back) p.ring[at < 0 ? at + cap : at] = id[u];
                 }
             }
-            if constexpr (PART == kPlanAll) {
+            if constexpr (SLOTS) {
                 // rows past max_tokens belong to requests that were refused
                 const int64_t left = p.max_tokens - s_row[i];
                 const int rows = static_cast<int>(left < 0 ? 0 : (s_req[i] < left ? s_req[i] : left));
@@ -233,21 +246,10 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
         }
         __syncthreads();
     }
-    if constexpr (PART == kPlanAll) {                    // input rows behind the last request's
+    if constexpr (SLOTS) {                    // input rows behind the last request's
         for (int64_t e = sums.rows * p.heads + tid; e < p.max_tokens * p.heads; e += NT) p.slots[e] = -1;
     }
-    if constexpr (PART == kPlanBehindSlots) {            // the slots' grid reads what these may overwrite
-        wait_for_stream();
-        if (tid < p.batch) p.seq_lens_out[tid] = len_out;            // batch <= NT
-    }
-    if (tid == 0) {
-        const int taken = s_taken;
-        const int64_t room = cap - count;
-        const int back = static_cast<int>(sums.gone < room ? sums.gone : room);
-        const int next = head + taken;
-        p.state_out[0] = next >= cap ? next - cap : next;
-        p.state_out[1] = count - taken + back;
-    }
+    if (tid == 0) write_state(p, ring, s_taken, sums.gone);
 }
 
 // The slots of a CTA's n tokens from the first slot of each, with coalesced stores.
@@ -266,20 +268,10 @@ __device__ __forceinline__ void write_slots(const PlanParams& p, int64_t t0, int
     }
 }
 
-// The first of n requests whose rows end after `token`.
-__device__ __forceinline__ int request_of(const int* ends, int n, int64_t token) {
-    int lo = 0;
-    while (lo < n) {
-        const int mid = (lo + n) >> 1;
-        if (ends[mid] <= token) lo = mid + 1; else n = mid;
-    }
-    return lo;
-}
-
-// Slots and table rows of larger calls of up to kSlotTile requests, before plan_kernel and beside it: a CTA per p.tile
+// Slots and table rows of larger calls of up to kSlotTile requests, before the rest of the plan: a CTA per p.tile
 // input rows that plans the whole batch for itself, which costs less than waiting for another kernel's plan (8 heads, 64
-// requests of 64 tokens: 3.3 us, 8.1 with the slots behind the plan; 116736 tokens: 5.6 and 10.3, with one or four times
-// kSlotTile rows to a CTA 6.7 and 5.9).  A new page is entered in its table row with its first token.
+// requests of 64 tokens: 3.3 us, 8.1 with the slots behind the plan; 116736 tokens: 5.0 and 10.3, with one or four times
+// kSlotTile rows to a CTA 5.4 and 5.8).  A new page is entered in its table row with its first token.
 __global__ void __launch_bounds__(kSlotTile) plan_slots_ahead_kernel(const PlanParams p) {
     __shared__ int64_t s_warp[kSlotTile / 32][2];
     __shared__ int64_t s_base[kSlotTile * kSlotTiles];
@@ -320,6 +312,49 @@ __global__ void __launch_bounds__(kSlotTile) plan_slots_ahead_kernel(const PlanP
     }
     __syncthreads();
     write_slots(p, t0, n, s_base);
+}
+
+// What is left of such a call, by one CTA that is launched behind plan_slots_ahead_kernel but runs beside it: that grid has
+// waited for all before it, nothing that it writes is read here, and what it reads is overwritten when it is done.
+__global__ void __launch_bounds__(kSlotTile) plan_beside_kernel(const PlanParams p) {
+    __shared__ int64_t s_warp[kSlotTile / 32][2];
+    __shared__ int s_gone[kSlotTile];
+    __shared__ int s_taken;
+    release_stream();
+    const int tid = threadIdx.x;
+    const int cap = p.num_pages;
+    const FreeRing ring(p);
+    if (tid == 0) {
+        s_taken = 0;
+        p.row_start[0] = 0;
+    }
+    PlanSums sums;
+    const PlannedRequest r = plan_request<kSlotTile>(p, 0, ring.count, sums, s_warp);
+    if (r.ok && r.need > 0) atomicMax(&s_taken, static_cast<int>(r.upto));
+    if (r.active) write_rows(p, tid, r);
+    s_gone[tid] = r.gone_end > cap ? cap : static_cast<int>(r.gone_end);
+    __syncthreads();
+    // the pages given back, one after the other
+    const int back = sums.gone < cap - ring.count ? static_cast<int>(sums.gone) : cap - ring.count;
+    for (int j0 = tid; j0 < back; j0 += kSlotTile * kCopies) {
+        int id[kCopies];
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+            const int j = j0 + u * kSlotTile;
+            if (j < back) {
+                const int b = request_of(s_gone, p.batch, j);
+                id[u] = p.table[static_cast<int64_t>(b) * p.width + j - (b ? s_gone[b - 1] : 0)];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+            const int j = j0 + u * kSlotTile, at = ring.count + j - (cap - ring.head);
+            if (j < back) p.ring[at < 0 ? at + cap : at] = id[u];
+        }
+    }
+    wait_for_stream();
+    if (r.active) p.seq_lens_out[tid] = plan_len(r);
+    if (tid == 0) write_state(p, ring, s_taken, sums.gone);
 }
 
 // The same for larger batches, after plan_kernel and by its results: one search per token for its request (in shared
