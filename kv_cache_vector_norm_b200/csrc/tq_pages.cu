@@ -236,6 +236,7 @@ struct SelectPlan {
     bool scored;                       // the keys are computed by a grid of their own, through the workspace
     int tile;                          // pages a CTA of that grid takes
     int room;                          // pages whose keys select_kernel keeps in shared memory
+    int parts;                         // its CTAs per row in the SCORED form
     size_t workspace_bytes;
 };
 
@@ -259,6 +260,9 @@ tq_status plan_select(const char* fn, const tq_select_args* a, SelectPlan* plan)
     const bool fits = key_stride(width) * 8 <= kSelSmem;
     plan->scored = !fits || (rows < device_sms() && width > 384);
     plan->room = plan->scored && key_stride(width) > kSortRoom ? kSortRoom : static_cast<int>(key_stride(width));
+    // several CTAs of select_kernel can make a row's choice only if they do not share its keys
+    plan->parts = 1;
+    while (plan->scored && plan->room == key_stride(width) && plan->parts < 8 && rows * plan->parts * 2 <= device_sms()) plan->parts *= 2;
     // two scoring CTAs to an SM with equal work, unless that leaves them little
     int64_t tile = (rows * width + 2 * device_sms() - 1) / (2 * device_sms());
     tile = (tile + 15) / 16 * 16;
@@ -283,7 +287,7 @@ tq_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaSt
     TQ_CUDA((prepare_kernel<kern>(kSortRoom * 8)), "tq_select_pages: cudaFuncSetAttribute");
     const unsigned tiles = (p.width + p.tile - 1) / p.tile;
     TQ_CUDA(launch(score_kernel<T, D>, grid * tiles, 1, kScoreThreads, 0, st, p), "tq_select_pages: score launch");
-    TQ_CUDA(launch(kern, grid, 1, kSortThreads, static_cast<size_t>(p.room) * 8, st, p), "tq_select_pages: launch");
+    TQ_CUDA(launch(kern, grid, p.parts, kSortThreads, static_cast<size_t>(p.room) * 8, st, p), "tq_select_pages: launch");
     return TQ_OK;
 }
 
@@ -330,6 +334,7 @@ extern "C" tq_status tq_select_pages(const tq_select_args* a, void* stream) {
     p.keep_last = a->keep_last;
     p.tile = plan.tile;
     p.room = plan.room;
+    p.parts = plan.parts;
     const int64_t rows = static_cast<int64_t>(a->batch) * a->num_kv_heads;
     p.keys = static_cast<uint32_t*>(a->workspace);
     p.sizes = plan.scored ? reinterpret_cast<float*>(p.keys + rows * key_stride(p.width)) : nullptr;

@@ -563,6 +563,7 @@ struct SelectParams {
     int heads, group, width, num_pages, budget, keep_first, keep_last;
     int tile;                          // pages a CTA of score_kernel scores
     int room;                          // pages whose keys and ids select_kernel's shared memory holds
+    int parts;                         // CTAs per row in select_kernel's SCORED form (a power of two, at most 8)
     uint32_t* keys;                    // [B][H_kv][key_stride]: keys of score_kernel (select_kernel's SCORED form)
     float* sizes;                      // [B][H_kv][tiles]: see score_pages
 };
@@ -727,19 +728,18 @@ __device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h
 }
 
 // The key of page `id` by its score in the defined order, by a whole warp: each 8 channels as an even and an odd chain,
-// the two added, then the upper half of the sums onto the lower.
+// the two added, then the upper half of the sums onto the lower.  q: the group's heads, in shared memory.
 template <typename T, int D>
-__device__ __forceinline__ uint32_t exact_key(const SelectParams& p, int b, int h, int id) {
+__device__ __forceinline__ uint32_t exact_key(const SelectParams& p, int h, int id, const uint4* q) {
     constexpr int LP = D / 8;                            // lanes with channels; the others repeat theirs
     const int l = (threadIdx.x & 31) % LP;
     const T* page = static_cast<const T*>(p.bounds) + (static_cast<int64_t>(id) * p.heads + h) * 2 * D;
-    const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<int64_t>(h) * p.group * D + 8 * l;
     const uint4 lw = __ldg(reinterpret_cast<const uint4*>(page + 8 * l)), hw = __ldg(reinterpret_cast<const uint4*>(page + D + 8 * l));
     const uint32_t lo[4] = {lw.x, lw.y, lw.z, lw.w}, hi[4] = {hw.x, hw.y, hw.z, hw.w};
     float best = -INFINITY;
 #pragma unroll 4
     for (int g = 0; g < p.group; ++g) {
-        const uint4 qw = __ldg(reinterpret_cast<const uint4*>(q + g * D));
+        const uint4 qw = q[g * LP + l];
         const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
         float even = 0.f, odd = 0.f;
 #pragma unroll
@@ -799,7 +799,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 // a bin goes in whole or holds one value.
 //
 // The work of one row is bound by the instructions of one SM, a few per key, so keys are read four at a time, what does
-// not compete has a key of its own (no tests of the page's index), and nothing is done per page that is left out.
+// not compete has a key of its own (no tests of the page's index), and nothing is done per page that is left out.  With
+// few rows several CTAs make a row's choice, each for itself, and write out a part of it (8 rows of 8192 pages: 16.7 us
+// with one, 15.8 with 4, 15.7 with 8, 16.0 with 16).
 template <typename T, int D, bool SCORED>
 __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : (D == 64 ? 4 : D == 128 ? 3 : 2))
     select_kernel(const SelectParams p) {
@@ -809,11 +811,12 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) uint32_t s_hist[kBins];
     __shared__ uint32_t s_pick[3];
-    __shared__ uint32_t s_warp[NW], s_warp2[NW];
+    __shared__ uint32_t s_warp[NW], s_warp2[NW], s_warp3[NW];
     __shared__ float s_size[NW];
     __shared__ uint32_t s_key[kList];
     __shared__ int s_page[kList];
     __shared__ int s_listed[2];                          // entries of the list; those above the bin
+    __shared__ uint4 s_q[8 * D / 8];                     // the group's heads
     begin_dependent();
     const int row = blockIdx.x;
     const int b = row / p.heads, h = row - b * p.heads;
@@ -823,32 +826,46 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
     int32_t* ids = reinterpret_cast<int32_t*>(keys + p.room);
     // what does not depend on the length is read while that is on its way
+    const int tiles = SCORED ? (p.width + p.tile - 1) / p.tile : 0;
+    float size = 0.f;
     if constexpr (SCORED) {
         const uint32_t* src = p.keys + row * key_stride(p.width);
 #pragma unroll 4
         for (int j = tid * 4; j < p.room; j += NT * 4)   // what lies behind the last key is overwritten below
             *reinterpret_cast<uint4*>(keys + j) = __ldcg(reinterpret_cast<const uint4*>(src + j));
-    } else {
-        for (int j = tid; j < p.width; j += NT) ids[j] = table[j];
+        if (tid < tiles) size = __ldcg(p.sizes + static_cast<int64_t>(row) * tiles + tid);
     }
+    const int known = p.width < p.room ? p.width : p.room;           // page ids in shared memory
+#pragma unroll 4
+    for (int j = tid; j < known; j += NT) {
+        if constexpr (SCORED)                            // not needed before the list is complete
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(ids + j)), "l"(table + j) : "memory");
+        else
+            ids[j] = table[j];
+    }
+    const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<int64_t>(h) * p.group * D;
+    for (int i = tid; i < p.group * D / 8; i += NT) s_q[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
     for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
     if (tid < 2) s_listed[tid] = 0;
     const int nb = static_cast<int>((len + kPage - 1) / kPage);
     int32_t* out = p.pages + static_cast<int64_t>(row) * p.budget;
     auto head_page = [&](int id) { return (id < 0 || id >= p.num_pages) ? -1 : id * p.heads + h; };
-    if (tid == 0) p.lens[row] = static_cast<int>(nb <= p.budget ? len : len - static_cast<int64_t>(nb - p.budget) * kPage);
+    const int part = SCORED ? blockIdx.y : 0;
+    if (tid == 0 && part == 0) p.lens[row] = static_cast<int>(nb <= p.budget ? len : len - static_cast<int64_t>(nb - p.budget) * kPage);
     if (nb <= p.budget) {                                // every page is kept
-        for (int j = tid; j < p.budget; j += NT) out[j] = head_page(j < nb ? table[j] : -1);
+        if (part == 0)
+            for (int j = tid; j < p.budget; j += NT) out[j] = head_page(j < nb ? table[j] : -1);
         return;
     }
-    float size = 0.f;
     const int padded = static_cast<int>(key_stride(nb));
+    auto id_of = [&](int j) { return SCORED && j >= known ? table[j] : ids[j]; };
     if constexpr (SCORED) {
         __syncthreads();
         // the passes over a very long sequence read the L2 cache
         if (padded > p.room) keys = p.keys + row * key_stride(p.width);
-        const int tiles = (p.width + p.tile - 1) / p.tile, used = (nb + p.tile - 1) / p.tile;
-        for (int i = tid; i < used; i += NT) size = fmaxf(size, __ldcg(p.sizes + static_cast<int64_t>(row) * tiles + i));
+        const int used = (nb + p.tile - 1) / p.tile;     // tiles with a page
+        if (tid >= used) size = 0.f;
+        for (int i = tid + NT; i < used; i += NT) size = fmaxf(size, __ldcg(p.sizes + static_cast<int64_t>(row) * tiles + i));
         for (int o = 16; o; o >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
     } else {
         __syncthreads();
@@ -869,20 +886,25 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
         }
     };
     const uint32_t wanted = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);   // of those that compete
-    // smallest and largest of a value over the block
+    uint32_t from = 0xffffffffu, bound = 0xffffffffu, need = 0;      // in: keys from `from` on, and `need` equal to `bound`
+    // The range of the block's keys; from each thread the smallest and largest of its own.
     auto block_range = [&](uint32_t& least, uint32_t& most) {
-        least = __reduce_min_sync(0xffffffffu, least);
-        most = __reduce_max_sync(0xffffffffu, most);
+        uint32_t low = __reduce_min_sync(0xffffffffu, least), high = __reduce_max_sync(0xffffffffu, most);
+        uint32_t best = __reduce_min_sync(0xffffffffu, most);
         __syncthreads();                                 // the sums before have been read
         if (lane == 0) {
-            s_warp[warp] = least;
-            s_warp2[warp] = most;
+            s_warp[warp] = low;
+            s_warp2[warp] = high;
+            s_warp3[warp] = best;
         }
         __syncthreads();
         least = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0xffffffffu);
         most = __reduce_max_sync(0xffffffffu, lane < NW ? s_warp2[lane] : 0u);
+        best = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp3[lane] : 0xffffffffu);
+        // every thread has a key from the smallest of the threads' largest ones on: if no more are wanted, it ends there
+        if (best > 0u && need <= NT) least = best - 1u;
+        --most;
     };
-    uint32_t from = 0xffffffffu, bound = 0xffffffffu, need = 0;      // in: keys from `from` on, and `need` equal to `bound`
     if (wanted > 0) {
         need = wanted;
         float error = s_size[lane < NW ? lane : 0];
@@ -899,7 +921,6 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
                     most = max(most, k + 1u);            // kKept: 0
                 });
                 block_range(least, most);
-                --most;
                 bound = least;
                 bits = 32 - __clz(static_cast<int>(most - least));
             }
@@ -955,19 +976,24 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
 #pragma unroll 1
             for (int j = j0; j < j1; j += kKeyGroup) {
                 const uint4 k4 = *reinterpret_cast<const uint4*>(keys + j);
-                const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+                const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w}, span = high - low;
+                unsigned some = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (k[i] >= low && k[i] <= high) {
-                        const int at = atomicAdd(&s_listed[0], 1);
-                        if (k[i] > top) atomicAdd(&s_listed[1], 1);
+                for (int i = 0; i < 4; ++i) some |= k[i] - low <= span ? 1u << i : 0u;
+                if (some) {
+#pragma unroll 1
+                    for (; some; some &= some - 1) {
+                        const int i = __ffs(some) - 1, at = atomicAdd(&s_listed[0], 1);
+                        const uint32_t key = keys[j + i];
+                        if (key > top) atomicAdd(&s_listed[1], 1);
                         if (at < kList) {
-                            s_key[at] = k[i];
+                            s_key[at] = key;
                             s_page[at] = j + i;
                         }
                     }
                 }
             }
+            if constexpr (SCORED) asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
             const int n = s_listed[0];
             // entries of the list that are in
@@ -985,7 +1011,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
 #pragma unroll 1
                     for (unsigned rest = __ballot_sync(0xffffffffu, k != 0u && k >= low && k <= high); rest; rest &= rest - 1) {
                         const int src = __ffs(rest) - 1;
-                        const uint32_t k2 = exact_key<T, D>(p, b, h, table[j - lane + src]);
+                        const uint32_t k2 = exact_key<T, D>(p, h, id_of(j - lane + src), s_q);
                         if (lane == src) now = k2;
                     }
                     keys[j] = now;
@@ -995,25 +1021,23 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
                 bits = 32;
                 continue;
             }
-            bool in = want > 0;
-            const int page = tid < n ? s_page[tid] : 0;
             if (want > 0 && want < n) {
 #pragma unroll 1
                 for (int x = warp; x < n; x += NW) {     // what is not a number (key 0) is so in any order
-                    const uint32_t k = s_key[x] ? exact_key<T, D>(p, b, h, table[s_page[x]]) : 0u;
+                    const uint32_t k = s_key[x] ? exact_key<T, D>(p, h, id_of(s_page[x]), s_q) : 0u;
                     __syncwarp();
                     if (lane == 0) s_key[x] = k;
                 }
                 __syncthreads();
-                if (tid < n) {
-                    const uint32_t mine = s_key[tid];
-                    int rank = 0;
-#pragma unroll 4
-                    for (int x = 0; x < n; ++x) rank += (s_key[x] > mine || (s_key[x] == mine && s_page[x] < page)) ? 1 : 0;
-                    in = rank < want;
-                }
             }
-            if (tid < n) keys[page] = in ? kKept : 0u;
+            for (int e = warp; e < n; e += NW) {         // a warp per entry: how many go before it
+                const uint32_t mine = s_key[e];
+                const int page = s_page[e];
+                int rank = 0;
+                for (int x = lane; x < n; x += 32) rank += (s_key[x] > mine || (s_key[x] == mine && s_page[x] < page)) ? 1 : 0;
+                rank = __reduce_add_sync(0xffffffffu, rank);
+                if (lane == 0) keys[page] = rank < want ? kKept : 0u;
+            }
             __syncthreads();
             from = high + 1;                             // high < 2^32 - 1
             need = 0;
@@ -1028,53 +1052,58 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     });
     n_in = __reduce_add_sync(0xffffffffu, n_in);
     n_tie = __reduce_add_sync(0xffffffffu, n_tie);
+    if constexpr (SCORED) asm volatile("cp.async.wait_all;" ::: "memory");   // if there was no list
     __syncthreads();                                     // the sums before have been read
     if (lane == 0) {
         s_warp[warp] = n_in;
         s_warp2[warp] = n_tie;
     }
     __syncthreads();
-    uint32_t in_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
-    uint32_t ties_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0u);
+    // the part's warps take equal runs of key groups, which begin in the chunk of warp `in_chunk` of the sums above
+    const int parts = SCORED ? p.parts : 1, groups = chunk / kKeyGroup, run = (groups + parts - 1) / parts;
+    const int part_end = (part + 1) * (NW / parts) * groups, g0 = part * (NW / parts) * groups + warp * run;
+    const int g1 = g0 + run < part_end ? g0 + run : part_end, in_chunk = g0 / groups;
+    uint32_t in_before = __reduce_add_sync(0xffffffffu, lane < in_chunk ? s_warp[lane] : 0u);
+    uint32_t ties_before = __reduce_add_sync(0xffffffffu, lane < in_chunk ? s_warp2[lane] : 0u);
+    const unsigned lower = (1u << lane) - 1u;            // the lanes before
 #pragma unroll 1
-    for (int j = j0; j - lane * 4 < j1; j += kKeyGroup) {
+    for (int g = g0 < part_end ? in_chunk * groups : g1; g < g1 && g * kKeyGroup < padded; ++g) {
+        const int j = g * kKeyGroup + lane * 4;
         const uint4 k4 = *reinterpret_cast<const uint4*>(keys + j);
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-        unsigned in = 0, tie = 0;                        // bit i: of the lane's i-th page
+        uint32_t i_at = in_before, t_at = ties_before;   // of the lane's first page
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            in |= k[i] >= from ? 1u << i : 0u;
-            tie |= k[i] < from && k[i] == bound ? 1u << i : 0u;
+            const unsigned in = __ballot_sync(0xffffffffu, k[i] >= from);
+            i_at += __popc(in & lower);
+            in_before += __popc(in);
         }
-        uint32_t sum = __popc(in) + (__popc(tie) << 16);
-        const uint32_t own = sum;
+        if (need) {                                      // else no key is a tie
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += t;
-        }
-        uint32_t i_at = in_before + ((sum - own) & 0xffffu), t_at = ties_before + ((sum - own) >> 16);
-#pragma unroll 1
-        for (unsigned rest = in | tie; rest; rest &= rest - 1) {
-            const int i = __ffs(rest) - 1;
-            const bool is_in = in >> i & 1u;
-            if (j + i < nb && (is_in || t_at < need)) {
-                const uint32_t at = i_at + (t_at < need ? t_at : need);
-                if (SCORED && at < static_cast<uint32_t>(p.room))
-                    ids[at] = j + i;                     // its id is looked up below
-                else
-                    out[at] = head_page(SCORED ? table[j + i] : ids[j + i]);
+            for (int i = 0; i < 4; ++i) {
+                const unsigned tie = __ballot_sync(0xffffffffu, k[i] < from && k[i] == bound);
+                t_at += __popc(tie & lower);
+                ties_before += __popc(tie);
             }
-            i_at += is_in ? 1u : 0u;
-            t_at += is_in ? 0u : 1u;
         }
-        sum = __shfl_sync(0xffffffffu, sum, 31);
-        in_before += sum & 0xffffu;
-        ties_before += sum >> 16;
-    }
-    if constexpr (SCORED) {
-        __syncthreads();
-        for (int i = tid; i < p.budget && i < p.room; i += NT) out[i] = head_page(table[ids[i]]);
+        if (g < g0) continue;
+        uint4 id4;                                       // ids of keys behind the last page are not used
+        if (!SCORED || j + 3 < p.room) {
+            id4 = *reinterpret_cast<const uint4*>(ids + j);
+        } else {
+            id4.x = j < nb ? table[j] : 0;
+            id4.y = j + 1 < nb ? table[j + 1] : 0;
+            id4.z = j + 2 < nb ? table[j + 2] : 0;
+            id4.w = j + 3 < nb ? table[j + 3] : 0;
+        }
+        const uint32_t id[4] = {id4.x, id4.y, id4.z, id4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool is_in = k[i] >= from, is_tie = !is_in && k[i] == bound && t_at < need;
+            if ((is_in || is_tie) && j + i < nb) out[i_at + (t_at < need ? t_at : need)] = head_page(static_cast<int>(id[i]));
+            i_at += is_in ? 1u : 0u;
+            t_at += is_tie ? 1u : 0u;
+        }
     }
 }
 

@@ -289,8 +289,25 @@ def test_select_bad_pages_and_numbers():
         check_select(q, bounds, table, [n * 16, n * 16 - 30], budget, 3, 1)
 
 
+@pytest.mark.parametrize("b", [1, 9, 18, 37, 80])
+@pytest.mark.parametrize("budget", [3, 90, 510, 517, 700])
+def test_select_long_rows_in_batches(b, budget):
+    """Rows of very different lengths, so few of them that several CTAs make a row's choice, or so many that one does; most
+    scores equal to others, and more or fewer pages wanted than the choice's CTA has threads."""
+    rng = np.random.default_rng(b + budget)
+    gen = torch.Generator(device=DEV).manual_seed(b + budget)
+    h, d, n, width = 2, 64, 1800, 1500
+    bounds = page_bounds(gen, n, h, d, torch.bfloat16)
+    bounds[::2] = bounds[torch.randint(0, 40, (n // 2,), generator=gen, device=DEV)]
+    table = np.stack([rng.permutation(n)[:width] for _ in range(b)])
+    lens = rng.integers(0, 16 * width + 40, b)
+    lens[0] = 16 * width - 3
+    q = torch.randn((b, h * 3, d), generator=gen, device=DEV).bfloat16()
+    check_select(q, bounds, table, lens, budget, 1, 1)
+
+
 def test_select_does_not_depend_on_the_call():
-    """A row gets the same pages alone (a cluster of CTAs) and in a large batch (one CTA), and on every run."""
+    """A row gets the same pages alone (in several CTAs) and in a large batch (one CTA), and on every run."""
     gen = torch.Generator(device=DEV).manual_seed(9)
     b, h, g, d, n = 40, 8, 4, 128, 1200
     bounds = page_bounds(gen, n, h, d, torch.float16)
