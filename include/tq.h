@@ -538,7 +538,8 @@ tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* by
  * of one kv head: a head page is a page of a pool with one kv head.  A listed page whose table entry names no page is
  * given as -1, which tq_attend_pages leaves out (tq_attend_decode needs entries that name pages).
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
- * result is the same on every run and for every shape of the call.  A score that is not a number ranks last.  (Not so
+ * result is the same on every run and for every shape of the call.  A score that is not a number ranks last; a NaN in
+ * the query counts as 0.  (Not so
  * where sum_c |q_c bounds_c| is past 2^126 or below 2^-100: which of the pages with such sums are kept is then undefined.)
  * Calls that overlap on the GPU must use distinct workspaces.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8, 2^39 pages or more in all rows).

@@ -650,16 +650,12 @@ __device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h
     constexpr int NC = D / 32;                           // 16-byte words of a row per lane
     constexpr int kBatch = NC < 4 ? NC : 4;              // of these, in flight at a time (for each of two rows, lo and hi)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    uint32_t pos[NC][4], neg[NC][4];                     // max(q, 0) and min(q, 0) of head gid
+    uint4 query[NC];                                     // of head gid
     {
         const T* q = static_cast<const T*>(p.q) + b * p.q_stride +
                      (static_cast<int64_t>(h) * p.group + (gid < p.group ? gid : p.group - 1)) * D + 8 * tig;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(q + 32 * c));
-            pos[c][0] = max2<T>(w.x, 0u); pos[c][1] = max2<T>(w.y, 0u); pos[c][2] = max2<T>(w.z, 0u); pos[c][3] = max2<T>(w.w, 0u);
-            neg[c][0] = min2<T>(w.x, 0u); neg[c][1] = min2<T>(w.y, 0u); neg[c][2] = min2<T>(w.z, 0u); neg[c][3] = min2<T>(w.w, 0u);
-        }
+        for (int c = 0; c < NC; ++c) query[c] = __ldg(reinterpret_cast<const uint4*>(q + 32 * c));
     }
     const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + 8 * tig;
     const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
@@ -690,7 +686,9 @@ __device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h
             }
 #pragma unroll
             for (int c = 0; c < kBatch; ++c) {
-                const uint32_t(&qp)[4] = pos[c0 + c], (&qn)[4] = neg[c0 + c];
+                const uint4 w = query[c0 + c];           // its two parts take no registers between the pages
+                const uint32_t qp[4] = {max2<T>(w.x, 0u), max2<T>(w.y, 0u), max2<T>(w.z, 0u), max2<T>(w.w, 0u)};
+                const uint32_t qn[4] = {min2<T>(w.x, 0u), min2<T>(w.y, 0u), min2<T>(w.z, 0u), min2<T>(w.w, 0u)};
                 const uint4 &l0 = lo[c][0], &l1 = lo[c][1], &h0 = hi[c][0], &h1 = hi[c][1];
                 mma16816<T>(s[0], h0.x, h1.x, h0.y, h1.y, qp[0], qp[1]);
                 mma16816<T>(s[1], h0.z, h1.z, h0.w, h1.w, qp[2], qp[3]);
@@ -801,9 +799,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 // The work of one row is bound by the instructions of one SM, a few per key, so keys are read four at a time, what does
 // not compete has a key of its own (no tests of the page's index), and nothing is done per page that is left out.  With
 // few rows several CTAs make a row's choice, each for itself, and write out a part of it (8 rows of 8192 pages: 16.7 us
-// with one, 15.8 with 4, 15.7 with 8, 16.0 with 16).
+// with one, 15.8 with 4, 15.7 with 8, 16.0 with 16).  Without SCORED two CTAs of an SM have the registers that the loads
+// want at d = 128 and 256 (512 rows of 200 pages at d = 128: 20.1 us; three CTAs 26.0), four at d = 64 (10.6; three 13.2).
 template <typename T, int D, bool SCORED>
-__global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : (D == 64 ? 4 : D == 128 ? 3 : 2))
+__global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : (D == 64 ? 4 : 2))
     select_kernel(const SelectParams p) {
     constexpr int NT = SCORED ? kSortThreads : kScoreThreads;
     constexpr int NW = NT / 32;
