@@ -97,6 +97,53 @@ def test_plan_writes_over_its_inputs(batch, heads, step, scarce):
     check_plan(new, lens, table, ring, [head, count], heads, int(np.maximum(new, 0).sum()), True)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("batch,heads", [(100, 8), (256, 2), (300, 4)])
+def test_plan_steps_without_a_pause(captured, batch, heads):
+    """Many steps of large calls one behind the other, each on the lengths, table and ring that the one before left, with
+    requests that finish and a pool too small for all."""
+    rng = np.random.default_rng(batch)
+    steps, width, rows = 24, 12, 4000
+    num_pages = batch * width // 3
+    news = [np.where(rng.random(batch) < 0.15, -1, rng.integers(0, 60, batch)) for _ in range(steps)]
+    state = dict(table=np.full((batch, width), -1, dtype=np.int64), ring=rng.permutation(num_pages), seq_lens=np.zeros(batch, dtype=np.int64),
+                 free_state=np.array([0, num_pages]))
+    t_table, t_ring, t_lens, t_state = i32(state["table"]), i32(state["ring"]), i32(state["seq_lens"]), i32(state["free_state"])
+    t_news = [i32(n) for n in news]
+    outs = [(torch.empty(rows * heads, dtype=torch.int64, device=DEV), torch.empty(batch + 1, dtype=torch.int32, device=DEV),
+             torch.empty(batch, dtype=torch.int32, device=DEV)) for _ in news]
+
+    def run():
+        for new, (slots, row_start, start_pos) in zip(t_news, outs):
+            tq.plan_pages(new, t_lens, t_table, t_ring, t_state, num_kv_heads=heads, slots=slots, row_start=row_start,
+                          start_pos=start_pos, seq_lens_out=t_lens, free_state_out=t_state)
+
+    if captured:
+        graph, kept = torch.cuda.CUDAGraph(), [t.clone() for t in (t_table, t_ring, t_lens, t_state)]
+        run()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            run()
+        for t, k in zip((t_table, t_ring, t_lens, t_state), kept):
+            t.copy_(k)
+        for o in outs:
+            o[0].fill_(-9)
+        graph.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    refused = 0
+    for new, (slots, row_start, start_pos) in zip(news, outs):
+        state = po.plan(new, state["seq_lens"], state["table"], state["ring"], state["free_state"], heads, rows)
+        refused += int(((state["start_pos"] < 0) & (new >= 0)).sum())
+        assert np.array_equal(slots.cpu().numpy(), state["slots"])
+        assert np.array_equal(row_start.cpu().numpy(), state["row_start"])
+        assert np.array_equal(start_pos.cpu().numpy(), state["start_pos"])
+    assert refused > batch
+    for t, name in ((t_table, "table"), (t_ring, "ring"), (t_lens, "seq_lens"), (t_state, "free_state")):
+        assert np.array_equal(t.cpu().numpy(), state[name]), name
+
+
 def test_plan_refuses_what_does_not_fit():
     # request 1 passes its table row, 3 the input rows (and so do all behind it), 5 finishes all the same
     lens, new = [10, 60, 0, 5, 20, 33], [6, 10, 16, 40, 1, -1]
