@@ -1575,8 +1575,8 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         advance<C::kRowCost>(p, seg, seg.pages - seg.pg);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    // only now: CTAs of the kernel behind this one that wait on an SM keep others of this grid's size from fitting when
-    // calls follow one another (64 ragged sequences at d = 64: 59.9 us with the release at the start, 50.6 us here)
+    // only now: CTAs of the kernel behind this one that wait on an SM can keep others of this grid's size from fitting when
+    // calls follow one another (64 ragged sequences at d = 64: 48.3 us, with the release at the start 48.8)
     release_stream();
 }
 
