@@ -350,13 +350,18 @@ namespace {
 template <int D>
 constexpr int min_share() { return PagesCfg<D>::kRowCost + PagesCfg<D>::kWarps; }
 
-// Table rows of at most this many pages are not split: a second launch takes longer than a CTA needs for them.  In one
-// kernel and in two, d = 128: 8 rows of 16 pages 5.2 and 7.5 us, of 32 7.5 and 7.7, of 48 9.6 and 7.7, of 64 11.9 and 7.7;
-// 512 rows of 32 26.3 and 29.5; d = 64, 512 rows of 64 30.9 and 28.1.
-constexpr int kDirectPages = 32;
+// Short table rows are not split: a second launch takes longer than a CTA needs for them.  A CTA of four warps takes rows
+// of up to 32 pages (d = 128, not split and split: 512 rows of 32 pages 26.5 and 29.5 us; d = 64, 512 rows of 64 30.9 and
+// 28.1); one of eight, in calls that leave every row an SM, up to 48 (8 rows of 48 pages: d = 128 7.8 and 7.6, d = 64 5.7 and
+// 6.9; of 64, d = 128: 9.4 and 7.6), or 64 if a split brings less than two SMs to a row (128 rows of 64: 10.1 and 12.8).
+// At d = 256 eight warps' pages do not fit.
+int direct_pages(int d, int64_t rows) {
+    const int sms = device_sms();
+    return d == 256 || rows > sms ? 32 : (2 * rows > sms ? 64 : 48);
+}
 
 struct PagesPlan {
-    bool direct;
+    bool direct, wide;
     int ctas, rows_join;
     size_t meta_bytes, workspace_bytes;
 };
@@ -379,26 +384,34 @@ tq_status plan_attend_pages(const char* fn, const tq_attend_pages_args* a, Pages
     TQ_NEED(cost < (1ll << 31), TQ_ERR_UNSUPPORTED, "%s: batch=%d with %d kv heads and max_blocks=%d holds 2^31 pages or more", fn,
             a->batch, a->num_kv_heads, a->max_blocks);
     const int rows = a->batch * a->num_kv_heads;
-    plan->direct = a->max_blocks <= kDirectPages;
-    plan->ctas = plan->direct ? rows : static_cast<int>(want < slots ? want : slots);
+    plan->direct = a->max_blocks <= direct_pages(d, rows);
+    plan->wide = plan->direct && d != 256 && rows <= device_sms();
+    const int shares = static_cast<int>(want < slots ? want : slots);
+    plan->ctas = plan->direct ? rows : shares;
     // the join goes by rows if there are no more of them than shares
-    plan->rows_join = !plan->direct && rows <= plan->ctas ? rows : 0;
-    if (plan->direct) {
-        plan->meta_bytes = plan->workspace_bytes = 0;
-        return TQ_OK;
-    }
-    plan->meta_bytes = static_cast<size_t>(plan->ctas) * sizeof(AttendPagesMeta);
-    plan->workspace_bytes = plan->meta_bytes + static_cast<size_t>(plan->ctas) * 2 * (16 + 8 * d) * 4;
+    plan->rows_join = !plan->direct && rows <= shares ? rows : 0;
+    // past 32 pages a workspace is asked for whether or not this call is split, so that whether a caller has to provide one
+    // depends on max_blocks alone
+    plan->meta_bytes = a->max_blocks <= 32 ? 0 : static_cast<size_t>(shares) * sizeof(AttendPagesMeta);
+    plan->workspace_bytes = a->max_blocks <= 32 ? 0 : plan->meta_bytes + static_cast<size_t>(shares) * 2 * (16 + 8 * d) * 4;
     return TQ_OK;
 }
 
+template <typename T, int D, bool WIDE>
+cudaError_t launch_attend_main(const AttendPagesParams& p, int ctas, cudaStream_t st) {
+    using C = PagesCfg<D, WIDE>;
+    constexpr auto kern = attend_pages_kernel<T, D, WIDE>;
+    const cudaError_t e = prepare_kernel<kern>(C::smem(8));
+    return e != cudaSuccess ? e : launch(kern, ctas, 1, C::kThreads, C::smem(p.group), st, p);
+}
+
 template <typename T, int D>
-tq_status launch_attend_pages(AttendPagesParams& p, int ctas, cudaStream_t st) {
-    using C = PagesCfg<D>;
+tq_status launch_attend_pages(AttendPagesParams& p, int ctas, bool wide, cudaStream_t st) {
     p.min_share = min_share<D>();
-    constexpr auto kern = attend_pages_kernel<T, D>;
-    TQ_CUDA((prepare_kernel<kern>(C::smem(8))), "tq_attend_pages: cudaFuncSetAttribute");
-    TQ_CUDA(launch(kern, ctas, 1, C::kThreads, C::smem(p.group), st, p), "tq_attend_pages: launch");
+    if constexpr (D != 256) {
+        if (wide) TQ_CUDA((launch_attend_main<T, D, true>(p, ctas, st)), "tq_attend_pages: launch");
+    }
+    if (!wide) TQ_CUDA((launch_attend_main<T, D, false>(p, ctas, st)), "tq_attend_pages: launch");
     if (!p.direct && ctas > 1)
         TQ_CUDA(launch(attend_pages_join_kernel<D>, p.rows_join ? p.rows_join : ctas - 1, (p.group + p.join_heads - 1) / p.join_heads,
                        p.rows_join ? kJoinThreads : p.join_heads * D /* four slices */, 0, st, p),
@@ -476,5 +489,5 @@ extern "C" tq_status tq_attend_pages(const tq_attend_pages_args* a, void* stream
     if (p.join_heads > p.group) p.join_heads = p.group;
     if (p.join_heads * a->head_dim / 4 > kJoinThreads) p.join_heads = kJoinThreads * 4 / a->head_dim;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_attend_pages, p, plan.ctas, st);
+    TQ_DISPATCH_TD(a->dtype, a->head_dim, launch_attend_pages, p, plan.ctas, plan.wide, st);
 }

@@ -1134,16 +1134,19 @@ struct AttendPagesMeta {
     int pad;
 };
 
-template <int D>
+// WIDE: calls of a few short rows, a CTA each, which have an SM for themselves.  A warp needs 0.6 us for a page then, not
+// for its bytes but for its chain of instructions, so there are twice as many warps (8 rows of 13 pages at d = 128: 4.2 us,
+// with four warps 5.0; of 32 pages 6.3 and 7.3).
+template <int D, bool WIDE = false>
 struct PagesCfg {
-    static constexpr int kWarps = 4;
+    static constexpr int kWarps = WIDE ? 8 : 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kPageBytes = kPage * D * 2;                 // one page of keys (or values) of a kv head
     // Pages of keys and values in flight per warp, 96 to 128 KB per SM.  More only lengthens the queues at the memory,
     // which SMs leave at different speeds while the shares are equal: 4, 3 and 3 pages at d = 64, 128 and 256 take
     // 50.6, 89.6 and 94.4 us where 2 take 48.0, 85.4 and 92.1 (64 ragged sequences, 131072 tokens, 64 selected pages).
     static constexpr int kStages = 2;
-    static constexpr int kCtasPerSm = (D == 64) ? 3 : (D == 128) ? 2 : 1;
+    static constexpr int kCtasPerSm = WIDE ? 1 : (D == 64) ? 3 : (D == 128) ? 2 : 1;
     static constexpr int kRing = kWarps * kStages * 2 * kPageBytes;
     // what a row costs besides its pages (its query, the joining of the warps' parts), in pages; a multiple of kWarps
     static constexpr int kRowCost = 8;
@@ -1231,24 +1234,24 @@ __device__ __forceinline__ void advance(const AttendPagesParams& p, PageCursor& 
 }
 
 // Attention of one new token over a paged cache.  softmax(scale q k^T) v needs every key and value once and a few
-// operations per byte, so the kernel is bound by how fast pages can be read, and the grid is laid out for that alone:
+// operations per byte, so a large call is bound by how fast pages can be read, and the grid is laid out for that alone:
 // all pages of the call, in the order (table row, kv head, page), are cut into shares of equal cost, one per resident
 // CTA, whatever the lengths of the sequences are.  A share covers parts of one or several rows (a row: one sequence
 // and kv head with its query heads, whose own cost counts as kRowCost pages); a row that lies inside one share is
 // finished there, and attend_pages_join_kernel joins the others.  Calls with short table rows take a CTA per row and
 // need no join.  The running maximum and sum (fp32) make the split exact up to rounding.
 //
-// Warp w of a CTA takes pages w, w + 4, ... of the share and keeps kStages of them in flight in its own ring of
+// Warp w of a CTA takes pages w, w + kWarps, ... of the share and keeps kStages of them in flight in its own ring of
 // shared memory with 16-byte cp.async copies, so no warp waits for another until a row ends.  16-byte chunk c of a
 // page's row r sits at chunk c ^ (r % 8): the copies and both ldmatrix reads are then free of bank conflicts.
 //   scores  S[head][token]  = q (A, 8 of 16 rows used) x k (B)
 //   values  O^T[col][head] += v^T (A) x p (B): the scores' fragment layout is that of p, nothing moves between lanes
 // p is 2^(s - m + 12) split into 16-bit terms (see Weights), so that rounding it costs no accuracy; with 8 heads or
 // fewer per row the tensor work is a small part of the time either way.
-template <typename T, int D>
-__global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm)
+template <typename T, int D, bool WIDE>
+__global__ void __launch_bounds__(PagesCfg<D, WIDE>::kThreads, PagesCfg<D, WIDE>::kCtasPerSm)
     attend_pages_kernel(const AttendPagesParams p) {
-    using C = PagesCfg<D>;
+    using C = PagesCfg<D, WIDE>;
     constexpr int S = C::kStages;
     constexpr int KS = D / 16;                           // k-steps of the scores, and 16-column tiles of the values
     constexpr float kPExp = 12.f;                        // weights carry 2^12 so that small ones keep their fp16 bits
@@ -1261,6 +1264,7 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
     const int G = p.group;
 
     wait_for_stream();
+    const bool direct = WIDE || p.direct;
     // ---- this CTA's share
     int x0 = 0, x1, share = INT_MAX;
     PageCursor seg;                                      // the first page at or behind x0
@@ -1274,7 +1278,7 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
             }
         }
     };
-    if (p.direct) {
+    if (direct) {
         seg.x = seg.pg = 0;
         seg.unit = blockIdx.x / p.mult;
         seg.m = blockIdx.x - seg.unit * p.mult;
@@ -1399,8 +1403,8 @@ __global__ void __launch_bounds__(PagesCfg<D>::kThreads, PagesCfg<D>::kCtasPerSm
         next_m = ld.m;
     }
     // while the first pages are on their way
-    if (!p.direct) write_zeros();
-    if (!p.direct && !p.rows_join && tid == 0) {
+    if (!direct) write_zeros();
+    if (!direct && !p.rows_join && tid == 0) {
         // the row that crosses into this share, if this is its first crossing
         const int row_begin = seg.x - seg.pg, first = row_begin / share;
         AttendPagesMeta m;

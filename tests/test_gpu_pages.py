@@ -432,6 +432,24 @@ def test_attend_pages_many_sequences(dtype, d, width, long):
     check_attend(q, kp, vp, table, lens)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("b,h,width", [(1, 1, 2), (1, 1, 48), (1, 1, 49), (37, 2, 48), (37, 2, 50), (74, 1, 49), (75, 1, 64), (75, 1, 65),
+                                       (148, 1, 20), (149, 1, 33), (148, 1, 64)])
+def test_attend_pages_where_the_split_begins(dtype, d, b, h, width):
+    """Rows few and short enough for a CTA each, with eight warps or four, and the first that are split."""
+    rng = np.random.default_rng(b + width)
+    gen = torch.Generator(device=DEV).manual_seed(b + width)
+    lens = rng.integers(0, 16 * width + 1, b)
+    lens[0], lens[-1] = 16 * width - 7, 16 * width
+    num_pages = int(sum(-(-lens // 16))) + 1
+    table, _ = random_table(rng, lens, width, num_pages)
+    kp, vp = pools(gen, num_pages, h, d, DTYPES[dtype])
+    forget_unused(kp, vp, table, lens)
+    q = torch.randn((b, h * 3, d), generator=gen, device=DEV).to(DTYPES[dtype])
+    check_attend(q, kp, vp, table, lens)
+
+
 def test_attend_pages_strided_operands_and_scale():
     rng = np.random.default_rng(3)
     gen = torch.Generator(device=DEV).manual_seed(3)
