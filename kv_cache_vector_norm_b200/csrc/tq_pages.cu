@@ -24,6 +24,12 @@ namespace {
         if (!(cond)) return fail(status, __VA_ARGS__);                                             \
     } while (0)
 
+// Whether n values at a and at b share no byte.
+bool apart(const int32_t* a, const int32_t* b, int64_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x + 4 * n <= y || y + 4 * n <= x;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // A limit on the pages of a pool and on a table's width: page indices, slots of a page and sums of two of them stay
@@ -143,21 +149,25 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     p.max_tokens = a->max_tokens;
     p.tile = kSlotTile;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // A decode step's few slots are written by the planning CTA itself, those of larger calls by a grid of their own: with
-    // 8 heads 64 requests of one token take 3.0 us in one kernel and 3.1 in two (and 2 us less on the host), 256 take 4.4
-    // and 3.4; past 256 requests, where that grid comes behind the plan, 512 take 6.4 and 7.8, 1024 take 10.3 and 7.2.  Up
-    // to 256 requests a CTA of 256 threads scans faster than one of 1024 (64 requests: 3.0 us, 5.4).
+    // Up to 256 requests the slots' grid plans for itself, and its first CTA does the rest if no output lies over an input
+    // (8 heads, 64 requests of one token: 2.4 us, of 64 tokens 2.8).
+    // Else the rest takes a second kernel, so a decode step's few slots are written by one planning CTA: with 8 heads 64
+    // requests of one token take 3.0 us in one kernel and 3.1 in two (and 2 us less on the host), 256 take 4.4 and 3.3.  Past
+    // 256 requests the slots come behind the plan: 512 take 6.4 us in one kernel and 7.8 in two, 1024 take 10.3 and 7.2.
+    // Up to 256 requests one CTA of 256 threads scans faster than one of 1024 (64 requests: 3.0 us, 5.4).
     const bool few = a->batch <= kSlotTile;
-    const int64_t tiles = (a->max_tokens + kSlotTile - 1) / kSlotTile;
-    if (a->max_tokens * a->num_kv_heads <= (few ? 1024 : 4096)) {
+    p.apart = few && apart(a->seq_lens, a->seq_lens_out, a->batch) && apart(a->free_state, a->free_state_out, 2);
+    const int64_t tiles = (a->max_tokens + kSlotTile - 1) / kSlotTile, each = (tiles + device_sms() - 1) / device_sms();
+    if (!p.apart && a->max_tokens * a->num_kv_heads <= (few ? 1024 : 4096)) {
         TQ_CUDA(few ? launch(plan_kernel<kSlotTile, true>, 1, 1, kSlotTile, 0, st, p)
                     : launch(plan_kernel<kPlanThreads, true>, 1, 1, kPlanThreads, 0, st, p),
                 "tq_plan_pages: launch");
     } else if (few) {
-        const int64_t each = (tiles + device_sms() - 1) / device_sms();
-        p.tile = kSlotTile * static_cast<int>(each < kSlotTiles ? each : kSlotTiles);
-        TQ_CUDA(launch(plan_slots_ahead_kernel, static_cast<unsigned>((a->max_tokens + p.tile - 1) / p.tile), 1, kSlotTile, 0, st, p), "tq_plan_pages: slot launch");
-        TQ_CUDA(launch(plan_beside_kernel, 1, 1, kSlotTile, 0, st, p), "tq_plan_pages: launch");
+        p.tile = kSlotTile * static_cast<int>(each < 1 ? 1 : (each < kSlotTiles ? each : kSlotTiles));
+        TQ_CUDA(launch(plan_slots_ahead_kernel, static_cast<unsigned>((a->max_tokens + p.tile - 1) / p.tile + (p.apart ? 1 : 0)), 1,
+                       kSlotTile, 0, st, p),
+                "tq_plan_pages: slot launch");
+        if (!p.apart) TQ_CUDA(launch(plan_beside_kernel, 1, 1, kSlotTile, 0, st, p), "tq_plan_pages: launch");
     } else {
         TQ_CUDA(launch(plan_kernel<kPlanThreads, false>, 1, 1, kPlanThreads, 0, st, p), "tq_plan_pages: launch");
         TQ_CUDA(launch(plan_slots_kernel, static_cast<unsigned>(tiles), 1, kSlotTile, 0, st, p), "tq_plan_pages: slot launch");

@@ -40,6 +40,7 @@ struct PlanParams {
     int batch, width, num_pages, heads;
     int64_t max_tokens;
     int tile;                          // tokens of a CTA of plan_slots_ahead_kernel
+    bool apart;                        // its first CTA does what plan_beside_kernel does otherwise
 };
 
 constexpr int kPlanThreads = 1024;      // requests a CTA of plan_kernel plans at a time, at most
@@ -268,17 +269,71 @@ __device__ __forceinline__ void write_slots(const PlanParams& p, int64_t t0, int
     }
 }
 
+// What plan_slots_ahead_kernel leaves of a call, by one CTA.  BESIDE: as a kernel of its own, which is launched behind that
+// grid but runs beside it: that grid has waited for all before it, nothing that it writes is read here, and what it reads
+// is overwritten when it is done.
+template <bool BESIDE>
+__device__ __forceinline__ void plan_rest(const PlanParams& p, int64_t (*s_warp)[2], int* s_gone) {
+    __shared__ int s_taken;
+    const int tid = threadIdx.x;
+    const int cap = p.num_pages;
+    const FreeRing ring(p);
+    if (tid == 0) {
+        s_taken = 0;
+        p.row_start[0] = 0;
+    }
+    PlanSums sums;
+    const PlannedRequest r = plan_request<kSlotTile>(p, 0, ring.count, sums, s_warp);
+    if (r.ok && r.need > 0) atomicMax(&s_taken, static_cast<int>(r.upto));
+    if (r.active) write_rows(p, tid, r);
+    s_gone[tid] = r.gone_end > cap ? cap : static_cast<int>(r.gone_end);
+    __syncthreads();
+    // the pages given back, one after the other
+    const int back = sums.gone < cap - ring.count ? static_cast<int>(sums.gone) : cap - ring.count;
+    for (int j0 = tid; j0 < back; j0 += kSlotTile * kCopies) {
+        int id[kCopies];
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+            const int j = j0 + u * kSlotTile;
+            if (j < back) {
+                const int b = request_of(s_gone, p.batch, j);
+                id[u] = p.table[static_cast<int64_t>(b) * p.width + j - (b ? s_gone[b - 1] : 0)];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+            const int j = j0 + u * kSlotTile, at = ring.count + j - (cap - ring.head);
+            if (j < back) p.ring[at < 0 ? at + cap : at] = id[u];
+        }
+    }
+    if constexpr (BESIDE) wait_for_stream();
+    if (r.active) p.seq_lens_out[tid] = plan_len(r);
+    if (tid == 0) write_state(p, ring, s_taken, sums.gone);
+}
+
+__global__ void __launch_bounds__(kSlotTile) plan_beside_kernel(const PlanParams p) {
+    __shared__ int64_t s_warp[kSlotTile / 32][2];
+    __shared__ int s_gone[kSlotTile];
+    release_stream();
+    plan_rest<true>(p, s_warp, s_gone);
+}
+
 // Slots and table rows of larger calls of up to kSlotTile requests, before the rest of the plan: a CTA per p.tile
 // input rows that plans the whole batch for itself, which costs less than waiting for another kernel's plan (8 heads, 64
 // requests of 64 tokens: 3.3 us, 8.1 with the slots behind the plan; 116736 tokens: 5.0 and 10.3, with one or four times
 // kSlotTile rows to a CTA 5.4 and 5.8).  A new page is entered in its table row with its first token.
+// If no output lies over an input (p.apart), the rest of the plan is the first CTA's (116736 tokens: 4.4 us).
 __global__ void __launch_bounds__(kSlotTile) plan_slots_ahead_kernel(const PlanParams p) {
     __shared__ int64_t s_warp[kSlotTile / 32][2];
     __shared__ int64_t s_base[kSlotTile * kSlotTiles];
     __shared__ int s_ends[kSlotTile], s_len[kSlotTile], s_from[kSlotTile];
     begin_dependent();
     const int tid = threadIdx.x;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tile;
+    if (p.apart && blockIdx.x == 0) {
+        plan_rest<false>(p, s_warp, s_ends);
+        return;
+    }
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x - (p.apart ? 1 : 0)) * p.tile;
     const int n = static_cast<int>(p.max_tokens - t0 < p.tile ? p.max_tokens - t0 : p.tile);
     const FreeRing ring(p);
     PlanSums sums;
@@ -312,49 +367,6 @@ __global__ void __launch_bounds__(kSlotTile) plan_slots_ahead_kernel(const PlanP
     }
     __syncthreads();
     write_slots(p, t0, n, s_base);
-}
-
-// What is left of such a call, by one CTA that is launched behind plan_slots_ahead_kernel but runs beside it: that grid has
-// waited for all before it, nothing that it writes is read here, and what it reads is overwritten when it is done.
-__global__ void __launch_bounds__(kSlotTile) plan_beside_kernel(const PlanParams p) {
-    __shared__ int64_t s_warp[kSlotTile / 32][2];
-    __shared__ int s_gone[kSlotTile];
-    __shared__ int s_taken;
-    release_stream();
-    const int tid = threadIdx.x;
-    const int cap = p.num_pages;
-    const FreeRing ring(p);
-    if (tid == 0) {
-        s_taken = 0;
-        p.row_start[0] = 0;
-    }
-    PlanSums sums;
-    const PlannedRequest r = plan_request<kSlotTile>(p, 0, ring.count, sums, s_warp);
-    if (r.ok && r.need > 0) atomicMax(&s_taken, static_cast<int>(r.upto));
-    if (r.active) write_rows(p, tid, r);
-    s_gone[tid] = r.gone_end > cap ? cap : static_cast<int>(r.gone_end);
-    __syncthreads();
-    // the pages given back, one after the other
-    const int back = sums.gone < cap - ring.count ? static_cast<int>(sums.gone) : cap - ring.count;
-    for (int j0 = tid; j0 < back; j0 += kSlotTile * kCopies) {
-        int id[kCopies];
-#pragma unroll
-        for (int u = 0; u < kCopies; ++u) {
-            const int j = j0 + u * kSlotTile;
-            if (j < back) {
-                const int b = request_of(s_gone, p.batch, j);
-                id[u] = p.table[static_cast<int64_t>(b) * p.width + j - (b ? s_gone[b - 1] : 0)];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kCopies; ++u) {
-            const int j = j0 + u * kSlotTile, at = ring.count + j - (cap - ring.head);
-            if (j < back) p.ring[at < 0 ? at + cap : at] = id[u];
-        }
-    }
-    wait_for_stream();
-    if (r.active) p.seq_lens_out[tid] = plan_len(r);
-    if (tid == 0) write_state(p, ring, s_taken, sums.gone);
 }
 
 // The same for larger batches, after plan_kernel and by its results: one search per token for its request (in shared

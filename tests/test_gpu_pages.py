@@ -98,8 +98,9 @@ def test_plan_writes_over_its_inputs(batch, heads, step, scarce):
 
 
 @pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("batch,heads", [(100, 8), (256, 2), (300, 4)])
-def test_plan_steps_without_a_pause(captured, batch, heads):
+def test_plan_steps_without_a_pause(captured, in_place, batch, heads):
     """Many steps of large calls one behind the other, each on the lengths, table and ring that the one before left, with
     requests that finish and a pool too small for all."""
     rng = np.random.default_rng(batch)
@@ -113,10 +114,14 @@ def test_plan_steps_without_a_pause(captured, batch, heads):
     outs = [(torch.empty(rows * heads, dtype=torch.int64, device=DEV), torch.empty(batch + 1, dtype=torch.int32, device=DEV),
              torch.empty(batch, dtype=torch.int32, device=DEV)) for _ in news]
 
-    def run():
+    other_lens, other_state = torch.empty_like(t_lens), torch.empty_like(t_state)
+
+    def run():                                           # an even number of steps: the last one ends in t_lens, t_state
+        lens, free, next_lens, next_free = t_lens, t_state, *((t_lens, t_state) if in_place else (other_lens, other_state))
         for new, (slots, row_start, start_pos) in zip(t_news, outs):
-            tq.plan_pages(new, t_lens, t_table, t_ring, t_state, num_kv_heads=heads, slots=slots, row_start=row_start,
-                          start_pos=start_pos, seq_lens_out=t_lens, free_state_out=t_state)
+            tq.plan_pages(new, lens, t_table, t_ring, free, num_kv_heads=heads, slots=slots, row_start=row_start,
+                          start_pos=start_pos, seq_lens_out=next_lens, free_state_out=next_free)
+            lens, free, next_lens, next_free = next_lens, next_free, lens, free
 
     if captured:
         graph, kept = torch.cuda.CUDAGraph(), [t.clone() for t in (t_table, t_ring, t_lens, t_state)]
