@@ -465,8 +465,8 @@ typedef struct tq_plan_args {
  *     ceil(len / 16) entries of its table row) are put at the ring's end, for later calls, and its length becomes 0.
  *   - Rows of refused requests, rows from row_start[batch] on, and rows whose table entry names no page get slot -1,
  *     which tq_encode_k, tq_encode_v and tq_append_pages skip.
- * Preconditions not checked: a page id is owned once (in one table row or in the ring), and seq_lens are those of
- * the table rows.  row_start saturates at 2^31 - 1 (requests from there on are refused).
+ * Preconditions not checked: a page id is owned once (in one table row or in the ring), seq_lens are those of the table
+ * rows, and no output overlaps an input but for the two pairs named above.  row_start saturates at 2^31 - 1 (requests from there on are refused).
  * Errors: TQ_ERR_INVALID_ARG for counts out of range, NULL or misaligned pointers.
  */
 tq_status tq_plan_pages(const tq_plan_args* args, void* stream);
