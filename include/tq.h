@@ -210,8 +210,8 @@ tq_status tq_decode_v(int d, int bits, int group, const uint8_t* data, const voi
  * contiguous layout; seq_lens is required for the paged layout).  The kernels clamp seq_lens[b] to
  * [0, max_seq_len] in the contiguous layout and to [0, max_blocks * block_size] in the paged one, so a length
  * past the cache attends to the whole addressable sequence and never reads beyond its rows or its
- * block-table row.  Every block_table entry below the (clamped) length must name a block of the pools.  Query head hq reads kv head
- * hq / (num_q_heads / num_kv_heads).
+ * block-table row.  Every block_table entry below the (clamped) length must name a block of the pools.  Rows of a
+ * pool behind a sequence's last token may hold anything.  Query head hq reads kv head hq / (num_q_heads / num_kv_heads).
  */
 typedef struct tq_attend_args {
     int batch;                 /* B >= 1 */

@@ -125,7 +125,9 @@ struct AttCfg {
     static constexpr int kSLutOff = kLutOff + (kLutAligned ? 2 : 1) * kLutBytes;
     static constexpr int kZsOff = kSLutOff + (QJL ? 1024 : 0);
     static constexpr int kBarOff = (kZsOff + kWarps * 8 * kVGroups * 4 + 15) & ~15;
-    static constexpr int kSmemMain = kBarOff + 8 * (2 * kStages) + 16;
+    // barriers, the abort flag, and per stage the tokens of its chunks
+    static constexpr int kTokOff = kBarOff + 8 * (2 * kStages) + 16;
+    static constexpr int kSmemMain = kTokOff + 16;
     // the window CTA reuses the same allocation
     static constexpr int kSmem = (kSmemMain > window_smem_floats<D>() * 4) ? kSmemMain : window_smem_floats<D>() * 4;
     static_assert(kNOff % 16 == 0 && kVOff % 16 == 0 && kSOff % 16 == 0 && kZOff % 16 == 0 && kSgOff % 16 == 0 &&
@@ -491,6 +493,10 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
     const uint32_t b_full = smem_u32(bars), b_empty = b_full + 8 * S;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * S);
+    // tokens that count in chunk c of stage s, byte 4 s + c: written by the producer before the stage is full.  (With each warp
+    // working its chunk's tokens out of the sequence's length instead, the kernel was 1 to 3 % slower.)
+    volatile uint8_t* const s_tokens = smem + C::kTokOff;
+    static_assert(C::kWarps == 4 && S <= 4, "a word per stage");
     // small key tables start on a multiple of their size, so an entry's address is (entry << 7) | lane bits
     const uint32_t lut_addr = C::kLutAligned
         ? (smem_u32(smem + C::kLutOff) + C::kLutBytes - 1) & ~static_cast<uint32_t>(C::kLutBytes - 1)
@@ -521,8 +527,9 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            // one expect-tx arrival by lane 0, or one cp.async arrival per lane of the producer warp (paged)
-            mbar_init(b_full + 8 * s, (p.block_table && C::kPagedCpAsync) ? 32 : 1);
+            // one expect-tx arrival by lane 0, or (paged) one by lane 0 for the stage's token counts and one cp.async
+            // arrival per lane of the producer warp
+            mbar_init(b_full + 8 * s, (p.block_table && C::kPagedCpAsync) ? 33 : 1);
             mbar_init(b_empty + 8 * s, C::kWarps);
         }
         *abort_flag = 0;
@@ -534,6 +541,17 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
 
     if (warp == C::kWarps) {
         // ------------------------------------------------------------------ copy producer
+        // the tokens of the last tile's chunks, a byte each: 16, fewer in the sequence's last one, 0 past the split's end
+        uint32_t tail = 0;
+        if (ntiles > 0) {
+            const int last = static_cast<int>(c_end - c_begin - (ntiles - 1) * C::kWarps) - 1;       // its last chunk
+            const int64_t left = T - (c_end - 1) * 16;
+            tail = 0x10101010u >> (8 * (C::kWarps - 1 - last));
+            if (left < 16) tail -= static_cast<uint32_t>(16 - left) << (8 * last);
+        }
+        auto put_tokens = [&](int64_t ti) {
+            reinterpret_cast<volatile uint32_t*>(s_tokens)[ti % S] = ti + 1 < ntiles ? 0x10101010u : tail;
+        };
         if (!p.block_table) {
             // contiguous cache: a stage's chunks are consecutive rows of the pool, one bulk copy per array (lane 0)
             if (lane == 0) {
@@ -544,6 +562,7 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
                     const int nc = static_cast<int>((c_end - c0 < C::kWarps) ? c_end - c0 : C::kWarps);
                     uint8_t* st = smem + s * C::kStageBytes;
                     const uint32_t bar = b_full + 8 * s;
+                    put_tokens(ti);
                     mbar_arrive_expect_tx(bar, nc * (C::kStageBytes / C::kWarps));
                     const int64_t row0 = (static_cast<int64_t>(b) * p.num_kv_heads + h) * p.max_seq_len + c0 * 16;
                     const int rows = nc * 16;
@@ -588,6 +607,10 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
 #pragma unroll
                 for (int c = 0; c < C::kWarps; ++c)
                     blks[c] = __shfl_sync(0xffffffffu, blk_cur, static_cast<int>(rel0 & 31) + c);
+                if (lane == 0) {
+                    put_tokens(ti);
+                    mbar_arrive(b_full + 8 * s);
+                }
                 auto blk_of = [&](int c) -> int32_t {
                     int32_t v = blks[0];
 #pragma unroll
@@ -626,9 +649,16 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
                 const int nc = static_cast<int>((c_end - c0 < C::kWarps) ? c_end - c0 : C::kWarps);
                 uint8_t* st = smem + s * C::kStageBytes;
                 const uint32_t bar = b_full + 8 * s;
+                const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks + c0;
+                int32_t blks[C::kWarps];
+#pragma unroll
+                for (int c = 0; c < C::kWarps; ++c) blks[c] = c < nc ? bt[c] : 0;
+                put_tokens(ti);
                 mbar_arrive_expect_tx(bar, nc * (C::kStageBytes / C::kWarps));
-                for (int c = 0; c < nc; ++c) {
-                    const int64_t blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + c0 + c];
+#pragma unroll
+                for (int c = 0; c < C::kWarps; ++c) {
+                    if (c >= nc) break;
+                    const int64_t blk = blks[c];
                     const int64_t row0 = (blk * p.num_kv_heads + h) * 16;
                     bulk_load(smem_u32(st + C::kKOff + c * 16 * C::kKRow), p.k_packed + row0 * C::kKRow,
                               16 * C::kKRow, bar);
@@ -701,14 +731,11 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
 
         // 32-bit loop state: a split holds fewer than 2^31 chunks
         const int ntiles32 = static_cast<int>(ntiles);
-        const int nrel = static_cast<int>(c_end - c_begin);
-        // tokens of the split's last chunk that belong to the sequence (16 for every other chunk)
-        const int last_valid = static_cast<int>(T - (c_end - 1) * 16);
         for (int ti = 0; ti < ntiles32; ++ti) {
             const int s = ti & (S - 1);
             if (!mbar_wait(b_full + 8 * s, static_cast<uint32_t>((ti / S) & 1), abort_flag)) break;
-            const int rel = ti * C::kWarps + warp;        // chunk index within the split
-            if (rel < nrel) {
+            const int tokens = s_tokens[4 * s + warp];     // of this warp's chunk
+            if (tokens) {
                 const uint8_t* const stg = smem + s * C::kStageBytes;
                 const uint8_t* const kch = st0 + s * C::kStageBytes;
                 // ---- scores: S'[16 x 8 tokens] per n-tile, rows gid (hi part) and gid+8 (lo part)
@@ -789,11 +816,16 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
                     lg[2] = fmaf((s2[1][0] + s2[1][2]) * unpre2, rh89.x, lg[2]);
                     lg[3] = fmaf((s2[1][1] + s2[1][3]) * unpre2, rh89.y, lg[3]);
                 }
-                if (rel == nrel - 1 && last_valid < 16) {          // the sequence's last, partial chunk
-                    lg[0] = (t0 < last_valid) ? lg[0] : -INFINITY;
-                    lg[1] = (t0 + 1 < last_valid) ? lg[1] : -INFINITY;
-                    lg[2] = (t0 + 8 < last_valid) ? lg[2] : -INFINITY;
-                    lg[3] = (t0 + 9 < last_valid) ? lg[3] : -INFINITY;
+                if (tokens < 16) {
+                    // the sequence's last, partial chunk.  Rows behind the last token may hold anything, and their weight 0
+                    // times NaN is NaN.  (This is the stage's last use, so no copy follows these writes.)
+                    uint16_t* const rows = reinterpret_cast<uint16_t*>(smem + s * C::kStageBytes) + (warp * 16 + tokens) * G8;
+                    for (int i = lane; i < (16 - tokens) * G8; i += 32) rows[C::kSOff / 2 + i] = rows[C::kZOff / 2 + i] = 0;
+                    __syncwarp();
+                    lg[0] = (t0 < tokens) ? lg[0] : -INFINITY;
+                    lg[1] = (t0 + 1 < tokens) ? lg[1] : -INFINITY;
+                    lg[2] = (t0 + 8 < tokens) ? lg[2] : -INFINITY;
+                    lg[3] = (t0 + 9 < tokens) ? lg[3] : -INFINITY;
                 }
                 const float lm = fmaxf(fmaxf(lg[0], lg[1]), fmaxf(lg[2], lg[3]));
                 if (__any_sync(0xffffffffu, lm > m_thr)) {

@@ -1,0 +1,129 @@
+"""Reading pages of a compressed cache: what lies behind a sequence's last token counts for nothing, and every reader takes the
+pages that a selection picked for each kv head.
+
+Attention is compared with 64-bit attention over the decoded pools by relative L2 error (L2_RTOL, the tolerance of the
+compressed cache's attention)."""
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_vector_norm_b200 import tq
+from oracle import pages_oracle as po
+from _tqh import L2_RTOL
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).to(DEV)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+class Compressed:
+    """Random rows in compressed pools of `rows` rows, whose codec has QJL residual keys or not."""
+
+    def __init__(self, rows, d, bits, v_bits, v_group, qjl=False, seed=0):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        x, y = torch.randn((2, rows, d), generator=gen, device=DEV).half()
+        self.d, self.rows, self.qjl, self.v_bits, self.v_group = d, rows, qjl, v_bits, v_group
+        self.signs = self.rho = None
+        if qjl:
+            self.codec = tq.QjlCodec(d, bits, 0)
+            packed, norms, self.signs, self.rho = self.codec.encode_k_qjl(x)
+        else:
+            self.codec = tq.Codec(d, bits, 0)
+            packed, norms = self.codec.encode_k(x)
+        self.cache = tq.Cache(packed, norms, *tq.encode_v(y, v_bits, v_group))
+        self.kw = dict(v_bits=v_bits, v_group=v_group)
+
+    def pools(self):
+        arrays = [self.cache.k_packed, self.cache.k_norms, self.cache.v_data, self.cache.v_scales, self.cache.v_zeros]
+        return arrays + ([self.signs, self.rho] if self.qjl else [])
+
+    def attend(self, q, h, **kw):
+        if self.qjl:
+            return tq.attend_decode_qjl(self.codec, q, self.cache, self.signs, self.rho, num_kv_heads=h, **self.kw, **kw)
+        return tq.attend_decode(self.codec, q, self.cache, num_kv_heads=h, **self.kw, **kw)
+
+    def decoded(self, h):
+        k = self.codec.decode_k(self.cache.k_packed, self.cache.k_norms, out_dtype=torch.float32)
+        v = tq.decode_v(self.cache.v_data, self.cache.v_scales, self.cache.v_zeros, self.d, self.v_bits, self.v_group,
+                        out_dtype=torch.float32)
+        return np64(k).reshape(-1, h, 16, self.d), np64(v).reshape(-1, h, 16, self.d)
+
+
+def spoil(t, rows):
+    """Bytes in rows of a pool that no code, norm or scale has reason to hold: NaN where the pool holds numbers."""
+    t[rows] = float("nan") if t.is_floating_point() else 0xA5
+
+
+FORMATS = [(64, 2, 2, 32, False), (64, 4, 4, 64, False), (64, 3, 4, 32, True), (128, 4, 4, 32, False), (128, 2, 8, 128, False),
+           (128, 6, 4, 32, False), (128, 3, 2, 32, True), (256, 4, 4, 32, True), (256, 3, 3, 256, False), (256, 4, 8, 32, False)]
+
+
+@pytest.mark.parametrize("d,bits,v_bits,v_group,qjl", FORMATS)
+@pytest.mark.parametrize("paged", [False, True])
+def test_rows_behind_the_last_token(d, bits, v_bits, v_group, qjl, paged):
+    """The same bits whatever the pools hold behind each sequence's last token: lengths that end inside a page, at one, in the
+    first and in a later one, one split and many."""
+    h, g, lens = 2, 3, [1, 15, 16, 0, 333, 2047, 2048]
+    b, width = len(lens), 128
+    c = Compressed(b * width * 16 * h, d, bits, v_bits, v_group, qjl)
+    q = torch.randn((b, h * g, d), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).half()
+    table = np.random.default_rng(0).permutation(b * width).reshape(b, width)
+    kw = dict(block_table=i32(table)) if paged else dict(max_seq_len=width * 16)
+    kw["seq_lens"] = i32(lens)
+    want = c.attend(q, h, **kw)
+    assert want.isfinite().all()
+    t = np.arange(width * 16)
+    for i, n in enumerate(lens):
+        for j in range(h):
+            row = (table[i, t // 16] * h + j) * 16 + t % 16 if paged else (i * h + j) * width * 16 + t
+            for pool in c.pools():
+                spoil(pool, torch.as_tensor(row[n:]).to(DEV))
+    assert torch.equal(c.attend(q, h, **kw), want)
+
+
+def selection(rng, b, h, n, pages, lens):
+    """Head pages of random pages for each (sequence, kv head), and the tokens of each list."""
+    ids = np.stack([[rng.permutation(pages)[:n] * h + j for j in range(h)] for _ in range(b)])
+    return ids, np.asarray(lens)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_every_reader_takes_selected_pages(d):
+    """attend_decode, attend_decode_noalloc, attend_decode_qjl and attend_scores on a list of pages per (sequence, kv head)."""
+    rng = np.random.default_rng(d)
+    b, h, g, n, num = 3, 2, 4, 11, 30
+    gen = torch.Generator(device=DEV).manual_seed(d)
+    q = torch.randn((b, h * g, d), generator=gen, device=DEV).half()
+    ids, lens = selection(rng, b, h, n, num, [[170, 176], [5, 0], [100, 161]])
+    kw = dict(block_table=i32(ids), seq_lens=i32(lens))
+    c = Compressed(num * h * 16, d, 4, 4, 32)
+    k, v = c.decoded(h)
+    ref, _ = po.attend(np64(q), k, v, ids, lens, d ** -0.5, True)
+    first = c.attend(q, h, **kw)
+    assert np.linalg.norm(np64(first) - ref) <= L2_RTOL * np.linalg.norm(ref)
+    assert not first[1, g:].any()
+    assert torch.equal(tq.attend_decode_noalloc(c.codec, q, c.cache, num_kv_heads=h, **c.kw, **kw), first)
+    scores = np64(tq.attend_scores(c.codec, q, c.cache, num_kv_heads=h, **c.kw, **kw))
+    assert scores.shape == (b, h * g, n * 16)
+    for i in range(b):
+        for j in range(h):
+            for x in range(g):
+                t = np.arange(lens[i, j])
+                want = k[ids[i, j, t // 16] // h, j, t % 16] @ np64(q)[i, j * g + x] * d ** -0.5
+                got = scores[i, j * g + x]
+                assert np.linalg.norm(got[:len(t)] - want) <= L2_RTOL * np.linalg.norm(want) and np.isneginf(got[len(t):]).all()
+    # residual keys: one list for every kv head gives what the table of those pages gives
+    c = Compressed(num * h * 16, d, 3, 4, 32, qjl=True)
+    pages = rng.permutation(num)[None, :n].repeat(b, 0)
+    lens = np.array([176, 3, 90])
+    whole = c.attend(q, h, block_table=i32(pages), seq_lens=i32(lens))
+    lists = np.stack([pages * h + j for j in range(h)], 1)
+    got = c.attend(q, h, block_table=i32(lists), seq_lens=i32(lens[:, None].repeat(h, 1)))
+    assert np.linalg.norm(np64(got - whole)) <= L2_RTOL * np.linalg.norm(np64(whole))
