@@ -210,7 +210,8 @@ tq_status tq_decode_v(int d, int bits, int group, const uint8_t* data, const voi
  * contiguous layout; seq_lens is required for the paged layout).  The kernels clamp seq_lens[b] to
  * [0, max_seq_len] in the contiguous layout and to [0, max_blocks * block_size] in the paged one, so a length
  * past the cache attends to the whole addressable sequence and never reads beyond its rows or its
- * block-table row.  Every block_table entry below the (clamped) length must name a block of the pools.  Rows of a
+ * block-table row.  A negative block_table entry names no block: its tokens are left out (of the
+ * softmax; their scores are -inf).  Every other entry below the (clamped) length must name a block of the pools.  Rows of a
  * pool behind a sequence's last token may hold anything.  Query head hq reads kv head hq / (num_q_heads / num_kv_heads).
  */
 typedef struct tq_attend_args {
@@ -429,8 +430,9 @@ tq_status tq_attend_decode_qjl(const tq_codec* codec, const tq_attend_args* args
  * page's keys, tq_select_pages picks pages by them, and either attention reads the picked ones.
  *
  * No call synchronises, allocates, or keeps anything between calls, so each can be captured into a CUDA graph and
- * replayed with new contents of the same buffers.  Page ids that name no page of a pool are never followed: their
- * tokens are left out.
+ * replayed with new contents of the same buffers.  Page ids that name no page of a pool are never followed by the calls
+ * below: their tokens are left out.  tq_attend_decode, which is not told how many blocks its pools hold, leaves out
+ * negative ids only.
  * ------------------------------------------------------------------------------------------------ */
 
 typedef struct tq_plan_args {
@@ -536,7 +538,7 @@ tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* by
  * so pages and lens are a block table and lengths with one row per (sequence, kv head).  Read them with
  * tq_attend_pages (selected = 1), or with tq_attend_decode on the compressed pools as batch * num_kv_heads sequences
  * of one kv head: a head page is a page of a pool with one kv head.  A listed page whose table entry names no page is
- * given as -1, which tq_attend_pages leaves out (tq_attend_decode needs entries that name pages).
+ * given as -1, which either attention leaves out.
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
  * result is the same on every run and for every shape of the call.  A score that is not a number ranks last; a NaN in
  * the query counts as 0.  (Not so

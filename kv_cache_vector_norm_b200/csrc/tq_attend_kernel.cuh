@@ -549,8 +549,13 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
             tail = 0x10101010u >> (8 * (C::kWarps - 1 - last));
             if (left < 16) tail -= static_cast<uint32_t>(16 - left) << (8 * last);
         }
-        auto put_tokens = [&](int64_t ti) {
-            reinterpret_cast<volatile uint32_t*>(s_tokens)[ti % S] = ti + 1 < ntiles ? 0x10101010u : tail;
+        auto put_tokens = [&](int64_t ti, uint32_t none) {                 // none: bytes of chunks that do not count
+            reinterpret_cast<volatile uint32_t*>(s_tokens)[ti % S] = (ti + 1 < ntiles ? 0x10101010u : tail) & ~none;
+        };
+        // A negative table entry names no block (a selection lists -1): its chunk has no tokens, and block 0 is copied in its
+        // place, so that every stage has the same copies.
+        auto no_block = [](const int32_t (&blks)[C::kWarps]) {
+            return (blks[0] >> 31 & 0xffu) | (blks[1] >> 31 & 0xff00u) | (blks[2] >> 31 & 0xff0000u) | (blks[3] >> 31 & 0xff000000u);
         };
         if (!p.block_table) {
             // contiguous cache: a stage's chunks are consecutive rows of the pool, one bulk copy per array (lane 0)
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
                     const int nc = static_cast<int>((c_end - c0 < C::kWarps) ? c_end - c0 : C::kWarps);
                     uint8_t* st = smem + s * C::kStageBytes;
                     const uint32_t bar = b_full + 8 * s;
-                    put_tokens(ti);
+                    put_tokens(ti, 0u);
                     mbar_arrive_expect_tx(bar, nc * (C::kStageBytes / C::kWarps));
                     const int64_t row0 = (static_cast<int64_t>(b) * p.num_kv_heads + h) * p.max_seq_len + c0 * 16;
                     const int rows = nc * 16;
@@ -608,9 +613,11 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
                 for (int c = 0; c < C::kWarps; ++c)
                     blks[c] = __shfl_sync(0xffffffffu, blk_cur, static_cast<int>(rel0 & 31) + c);
                 if (lane == 0) {
-                    put_tokens(ti);
+                    put_tokens(ti, no_block(blks));
                     mbar_arrive(b_full + 8 * s);
                 }
+#pragma unroll
+                for (int c = 0; c < C::kWarps; ++c) blks[c] = max(blks[c], 0);
                 auto blk_of = [&](int c) -> int32_t {
                     int32_t v = blks[0];
 #pragma unroll
@@ -653,12 +660,12 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB, VG, QJL>::kThreads, AttCfg<D
                 int32_t blks[C::kWarps];
 #pragma unroll
                 for (int c = 0; c < C::kWarps; ++c) blks[c] = c < nc ? bt[c] : 0;
-                put_tokens(ti);
+                put_tokens(ti, no_block(blks));
                 mbar_arrive_expect_tx(bar, nc * (C::kStageBytes / C::kWarps));
 #pragma unroll
                 for (int c = 0; c < C::kWarps; ++c) {
                     if (c >= nc) break;
-                    const int64_t blk = blks[c];
+                    const int64_t blk = max(blks[c], 0);
                     const int64_t row0 = (blk * p.num_kv_heads + h) * 16;
                     bulk_load(smem_u32(st + C::kKOff + c * 16 * C::kKRow), p.k_packed + row0 * C::kKRow,
                               16 * C::kKRow, bar);
@@ -1019,9 +1026,12 @@ __global__ void __launch_bounds__(128) attend_scores_kernel(const AttendParams p
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint4* qf = p.qfrag + (static_cast<int64_t>(b) * p.num_kv_heads + h) * p.qfrag_stride;
     const float unpre = __ldcg(reinterpret_cast<const float*>(qf + KS * 32) + gid);
-    const int64_t T = attend_seq_len(p, b);
     const int64_t chunk = static_cast<int64_t>(blockIdx.x) * 4 + warp;
     if (chunk * 16 >= score_len) return;
+    int64_t T = attend_seq_len(p, b);
+    int block = 0;
+    if (p.block_table && chunk * 16 < T) block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + chunk];
+    if (block < 0) T = 0;                                  // the entry names no block: its tokens are left out
     // this lane's quarter of the key rows of tokens 8 nt + gid (zero past the sequence)
     uint32_t w[2][kQuarterWords];
     float nrm[2];
@@ -1032,9 +1042,8 @@ __global__ void __launch_bounds__(128) attend_scores_kernel(const AttendParams p
         for (int i = 0; i < kQuarterWords; ++i) w[nt][i] = 0u;
         nrm[nt] = 0.f;
         if (tk < T) {
-            const int64_t row = p.block_table
-                ? (static_cast<int64_t>(p.block_table[static_cast<int64_t>(b) * p.max_blocks + tk / 16]) * p.num_kv_heads + h) * 16 + tk % 16
-                : (static_cast<int64_t>(b) * p.num_kv_heads + h) * p.max_seq_len + tk;
+            const int64_t row = p.block_table ? (static_cast<int64_t>(block) * p.num_kv_heads + h) * 16 + tk % 16
+                                              : (static_cast<int64_t>(b) * p.num_kv_heads + h) * p.max_seq_len + tk;
             const uint16_t* k16 = reinterpret_cast<const uint16_t*>(p.k_packed + row * kKRow) + tig * kQuarterHalves;
 #pragma unroll
             for (int i = 0; i < kQuarterWords; ++i) {

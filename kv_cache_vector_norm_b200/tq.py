@@ -455,7 +455,8 @@ def attend_decode(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv_heads: 
                   win_v: torch.Tensor | None = None, win_lens: torch.Tensor | None = None) -> torch.Tensor:
     """One decode step: q [B, H_q, d] fp16 against the compressed cache, plus (win_k, win_v: [B, H_kv, W, d]
     fp16, win_lens: [B] int32 or None) a window of recent uncompressed tokens.  Returns out [B, H_q, d] f32.
-    block_table [B, H_kv, n] with seq_lens [B, H_kv] (select_pages) attends to the selected pages of a paged cache."""
+    block_table [B, H_kv, n] with seq_lens [B, H_kv] (select_pages) attends to the selected pages of a paged cache.  Negative
+    entries of a block table are left out; all others up to a row's length must name pages of the cache."""
     _need_cuda(q, "q", torch.float16)
     kw = dict(num_kv_heads=num_kv_heads, v_bits=v_bits, v_group=v_group, max_seq_len=max_seq_len,
               block_table=block_table, seq_lens=seq_lens, scale=scale)
@@ -603,7 +604,8 @@ def select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
                  lens: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """The `budget` pages of each (sequence, kv head) whose bounds allow the largest q . k (the first keep_first and
     last keep_last always): (pages int32 [B, H_kv, budget] of head pages, lens int32 [B, H_kv]), to be passed as
-    block_table and seq_lens to attend_pages or attend_decode.  workspace: scratch of 5 * B * H_kv * (max_blocks + 127)
+    block_table and seq_lens to attend_pages or attend_decode.  A listed page whose table entry names no page of bounds is -1,
+    and both leave its tokens out.  workspace: scratch of 5 * B * H_kv * (max_blocks + 127)
     bytes is always enough (a call with few rows allocates what it needs if it is not given)."""
     if bounds.dim() != 4:
         raise ValueError("bounds must be [num_pages, H_kv, 2, d]")

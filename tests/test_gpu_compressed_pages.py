@@ -127,3 +127,68 @@ def test_every_reader_takes_selected_pages(d):
     lists = np.stack([pages * h + j for j in range(h)], 1)
     got = c.attend(q, h, block_table=i32(lists), seq_lens=i32(lens[:, None].repeat(h, 1)))
     assert np.linalg.norm(np64(got - whole)) <= L2_RTOL * np.linalg.norm(np64(whole))
+
+
+@pytest.mark.parametrize("d,bits,v_bits,v_group,qjl", FORMATS)
+@pytest.mark.parametrize("b,n", [(2, 5), (3, 40), (1, 700)])
+def test_negative_entries_are_left_out(d, bits, v_bits, v_group, qjl, b, n):
+    """Entries of -1 (and other negative ones) at the start, inside and at the end of a row, for whole rows, for a whole stage
+    of the copies; few pages and so many that the rows are split and block ids are read in several rounds."""
+    rng = np.random.default_rng(d + n)
+    h, g, num = 2, 3, n + 9
+    c = Compressed(num * h * 16, d, bits, v_bits, v_group, qjl)
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q = torch.randn((b, h * g, d), generator=gen, device=DEV).half()
+    table = np.stack([rng.permutation(num)[:n] for _ in range(b)])
+    table[0, [0, n // 2, n - 1]] = [-1, -7, -2 ** 31]
+    table[0, 4:8] = -1
+    if b > 1:
+        table[1] = -1
+    if b > 2:
+        table[2, rng.random(n) < 0.4] = -1
+    lens = np.array([16 * n - 5, 16 * n - 16, 16 * n][:b])
+    got = np64(c.attend(q, h, block_table=i32(table), seq_lens=i32(lens)))
+    assert np.isfinite(got).all()
+    if b > 1:
+        assert not got[1].any()
+    if not qjl:
+        k, v = c.decoded(h)
+        ref, _ = po.attend(np64(q), k, v, table, lens, d ** -0.5)
+        assert np.linalg.norm(got - ref) <= L2_RTOL * np.linalg.norm(ref)
+        lists = np.stack([np.where(table < 0, -1, table * h + j) for j in range(h)], 1)
+        sel = np64(c.attend(q, h, block_table=i32(lists), seq_lens=i32(lens[:, None].repeat(h, 1))))
+        assert np.linalg.norm(sel - ref) <= L2_RTOL * np.linalg.norm(ref)
+        scores = tq.attend_scores(c.codec, q, c.cache, num_kv_heads=h, **c.kw, block_table=i32(table), seq_lens=i32(lens))
+        there = (table.repeat(16, 1) >= 0) & (np.arange(16 * n) < lens[:, None])
+        assert np.array_equal(np.isfinite(np64(scores)), there[:, None].repeat(h * g, 1))
+        return
+    # residual keys: the same pages in the same order without the others, whose last one is whole
+    lens[:] = 16 * n
+    got = np64(c.attend(q, h, block_table=i32(table), seq_lens=i32(lens)))
+    short = np.full((b, n), 0)
+    for i in range(b):
+        good = table[i][table[i] >= 0]
+        short[i, :len(good)], lens[i] = good, 16 * len(good)
+    ref = np64(c.attend(q, h, block_table=i32(short), seq_lens=i32(lens)))
+    assert np.linalg.norm(got - ref) <= L2_RTOL * np.linalg.norm(ref)
+
+
+def test_a_selection_with_pages_that_are_none():
+    """First and last pages are listed whatever their table entry names: the -1 that a selection gives for them goes through
+    attention over compressed pages."""
+    rng = np.random.default_rng(5)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    b, h, g, d, n, num, budget = 3, 2, 4, 128, 30, 100, 8
+    c = Compressed(num * h * 16, d, 4, 4, 32)
+    k, v = c.decoded(h)
+    keys = torch.as_tensor(k, device=DEV).half()
+    bounds = torch.stack((keys.amin(2), keys.amax(2)), 2).contiguous()
+    table = np.stack([rng.permutation(num)[:n] for _ in range(b)])
+    table[0, 0], table[1, n - 1], table[2, 3] = -1, num + 3, -1
+    lens = np.array([16 * n - 3, 16 * n - 9, 70])
+    q = torch.randn((b, h * g, d), generator=gen, device=DEV).half()
+    pages, tokens = tq.select_pages(q, bounds, i32(table), i32(lens), budget=budget)
+    assert (pages[0, :, 0] == -1).all() and (pages[1, :, budget - 1] == -1).all() and (pages[2, :, 3] == -1).all()
+    got = np64(c.attend(q, h, block_table=pages, seq_lens=tokens))
+    ref, _ = po.attend(np64(q), k, v, pages.cpu().numpy(), tokens.cpu().numpy(), d ** -0.5, True)
+    assert np.linalg.norm(got - ref) <= L2_RTOL * np.linalg.norm(ref)
