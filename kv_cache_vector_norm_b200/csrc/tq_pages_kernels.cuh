@@ -16,7 +16,8 @@ constexpr int kPage = 16;
 
 // Every kernel here is launched as a programmatic dependent of what precedes it in the stream.  It begins by waiting
 // until all of that is complete and visible, and lets the kernel behind it be scheduled early (which waits in turn), so
-// that a step's launches do not each add their latency.
+// that a step's launches do not each add their latency.  What it reads may be written while it is already resident, so it
+// loads nothing through the non-coherent path, which is for data that is read-only as long as the grid lives.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_stream() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void begin_dependent() {
@@ -667,7 +668,7 @@ __device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h
         const T* q = static_cast<const T*>(p.q) + b * p.q_stride +
                      (static_cast<int64_t>(h) * p.group + (gid < p.group ? gid : p.group - 1)) * D + 8 * tig;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) query[c] = __ldg(reinterpret_cast<const uint4*>(q + 32 * c));
+        for (int c = 0; c < NC; ++c) query[c] = *reinterpret_cast<const uint4*>(q + 32 * c);
     }
     const T* bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(h) * 2 * D + 8 * tig;
     const int64_t page_stride = static_cast<int64_t>(p.heads) * 2 * D;
@@ -691,8 +692,8 @@ __device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h
                 for (int r = 0; r < 2; ++r) {
                     lo[c][r] = hi[c][r] = make_uint4(0u, 0u, 0u, 0u);
                     if (there[r]) {
-                        lo[c][r] = __ldg(reinterpret_cast<const uint4*>(src[r] + 32 * (c0 + c)));
-                        hi[c][r] = __ldg(reinterpret_cast<const uint4*>(src[r] + 32 * (c0 + c) + D));
+                        lo[c][r] = *reinterpret_cast<const uint4*>(src[r] + 32 * (c0 + c));
+                        hi[c][r] = *reinterpret_cast<const uint4*>(src[r] + 32 * (c0 + c) + D);
                     }
                 }
             }
@@ -744,7 +745,7 @@ __device__ __forceinline__ uint32_t exact_key(const SelectParams& p, int h, int 
     constexpr int LP = D / 8;                            // lanes with channels; the others repeat theirs
     const int l = (threadIdx.x & 31) % LP;
     const T* page = static_cast<const T*>(p.bounds) + (static_cast<int64_t>(id) * p.heads + h) * 2 * D;
-    const uint4 lw = __ldg(reinterpret_cast<const uint4*>(page + 8 * l)), hw = __ldg(reinterpret_cast<const uint4*>(page + D + 8 * l));
+    const uint4 lw = *reinterpret_cast<const uint4*>(page + 8 * l), hw = *reinterpret_cast<const uint4*>(page + D + 8 * l);
     const uint32_t lo[4] = {lw.x, lw.y, lw.z, lw.w}, hi[4] = {hw.x, hw.y, hw.z, hw.w};
     float best = -INFINITY;
 #pragma unroll 4
@@ -855,7 +856,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
             ids[j] = table[j];
     }
     const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<int64_t>(h) * p.group * D;
-    for (int i = tid; i < p.group * D / 8; i += NT) s_q[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+    for (int i = tid; i < p.group * D / 8; i += NT) s_q[i] = reinterpret_cast<const uint4*>(q)[i];
     for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
     if (tid < 2) s_listed[tid] = 0;
     const int nb = static_cast<int>((len + kPage - 1) / kPage);
@@ -1375,7 +1376,7 @@ __global__ void __launch_bounds__(PagesCfg<D, WIDE>::kThreads, PagesCfg<D, WIDE>
     PageCursor ld = seg;                                 // the next page to be copied
     if (first_of(seg.x)) advance<C::kRowCost>(p, ld, first_of(seg.x));
     auto page_id = [&]() -> int {
-        return ld.x < x1 ? __ldg(p.table + static_cast<int64_t>(ld.unit) * p.width + ld.pg) : -1;
+        return ld.x < x1 ? p.table[static_cast<int64_t>(ld.unit) * p.width + ld.pg] : -1;
     };
     unsigned good = 0;                                   // bit s: stage s holds a page (its id named one)
     auto issue = [&](int s, int id, int m) {
@@ -1443,8 +1444,8 @@ __global__ void __launch_bounds__(PagesCfg<D, WIDE>::kThreads, PagesCfg<D, WIDE>
             const T* q = static_cast<const T*>(p.q) + b * p.q_stride + (static_cast<int64_t>(h) * G + gid) * D + 2 * tig;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t a = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks)) : 0u;
-                const uint32_t c = gid < G ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8)) : 0u;
+                const uint32_t a = gid < G ? *reinterpret_cast<const uint32_t*>(q + 16 * ks) : 0u;
+                const uint32_t c = gid < G ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8) : 0u;
                 if constexpr (C::kQueryInSmem) {
                     qs[ks * 32] = make_uint2(a, c);      // read back by this lane only
                 } else {

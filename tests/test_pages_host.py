@@ -173,3 +173,14 @@ def test_select_and_attend_by_hand():
     out, err = po.attend(np.array(q, dtype=np.float64), k, v, np.array([[0, 1]]), [17], 1.0)
     assert np.allclose(out, (16 * 1 + 3 * 5) / 19) and err.max() < 1e-3
     assert not po.attend(np.array(q, dtype=np.float64), k, v, np.array([[0, 1]]), [0], 1.0)[0].any()
+
+
+def test_kernels_that_start_early_load_coherently():
+    """The paged cache's kernels are resident while the work before them still writes what they read: none of their loads is a
+    non-coherent one (__ldg, ld.global.nc, or a const __restrict__ pointer, which the compiler may load that way)."""
+    import os
+    with open(os.path.join(os.path.dirname(tq.__file__), "csrc", "tq_pages_kernels.cuh")) as f:
+        text = f.read()
+    assert "griddepcontrol.wait" in text
+    for what in ("__ldg(", ".nc.", "__restrict__"):
+        assert what not in text, what
