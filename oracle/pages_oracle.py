@@ -167,3 +167,22 @@ def attend(q, k_pool, v_pool, table, seq_lens, scale, selected=False):
                 sums = 2 * (len(keys) / 16 + 64) * 2.0 ** -23
                 err[i, j * g + x] = np.abs(values).max() * (2 * logit + 2.0 ** -20 + sums)
     return out, err
+
+
+# Relative L2 error of an attention output row (row_error) that 32-bit arithmetic stays below on ordinary inputs: queries, keys and
+# values of about unit normal entries, at most 256 channels, scale d^-0.5.  A row is sum p_t v_t / sum p_t with values of random
+# signs, so an error e_t of the t-th weight, relative to it, comes out as the root mean square of the e_t weighted with p_t^2.
+# Their parts, per weight:
+#   the logit: at most 256 / 16 steps of sums cut off behind 24 bits, each below 2^-23 of a partial sum that stays around
+#     sqrt(d) / 2 times the scale: 16 * 2^-24 on average with one sign, 1.0e-6; in two chains half of it, 0.5e-6
+#   its scaling and the subtraction of the maximum, of numbers up to 8: 2 * 2^-24 * 8 / sqrt(3), 0.6e-6
+#   the exponential, 2^-22: 0.2e-6; two fp16 or three bf16 terms of a weight, 2^-23: 0.1e-6
+#   the sums over tokens and their join, rounded in 32 bits: 16 tokens at a time, 2^-24 sqrt(300): 1.0e-6
+# together (adding up) 2.4e-6.  Weights of 11 bits are off by 2^-12 / sqrt(3) = 1.4e-4, of 16 bits, cut off, by up to 2^-16 = 1.5e-5.
+ROW_RTOL = 3e-6
+
+
+def row_error(got, want):
+    """Relative L2 error of each output row [..., d] (0 where both rows are zero)."""
+    size = np.linalg.norm(want, axis=-1)
+    return np.linalg.norm(got - want, axis=-1) / np.where(size == 0, 1, size)

@@ -184,3 +184,28 @@ def test_kernels_that_start_early_load_coherently():
     assert "griddepcontrol.wait" in text
     for what in ("__ldg(", ".nc.", "__restrict__"):
         assert what not in text, what
+
+
+@pytest.mark.parametrize("d,n", [(64, 200), (128, 1800), (256, 700)])
+@pytest.mark.parametrize("kind,terms,passes", [("fp16", 1, False), ("fp16", 2, True), ("bf16", 2, False), ("bf16", 3, True)])
+def test_row_tolerance_tells_the_weights_apart(d, n, kind, terms, passes):
+    """Weights of one term too few (11 or 16 bits) miss the tolerance of attention over uncompressed pages, the kernels' own do
+    not come near it."""
+    rng = np.random.default_rng(d + n)
+    got, want = [], []
+    for _ in range(8):
+        q, k, v = (rng.standard_normal(s).astype(np.float16).astype(np.float64) for s in ((d,), (n, d), (n, d)))
+        s = k @ q / np.sqrt(d) * np.log2(np.e)
+        p = np.exp2(s - s.max() + 12)
+        rest, weights = p.astype(np.float32), np.zeros(n)
+        for _ in range(terms):
+            if kind == "fp16":
+                term = rest.astype(np.float16).astype(np.float32)
+            else:
+                term = (rest.view(np.uint32) & np.uint32(0xffff0000)).view(np.float32)
+            weights += term
+            rest = rest - term
+        got.append(weights @ v / p.sum())
+        want.append(p @ v / p.sum())
+    err = po.row_error(np.stack(got), np.stack(want)).max()
+    assert err <= po.ROW_RTOL / 10 if passes else err > 2 * po.ROW_RTOL
