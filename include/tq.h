@@ -541,8 +541,9 @@ tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* by
  * given as -1, which either attention leaves out.
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
  * result is the same on every run and for every shape of the call.  A score that is not a number ranks last; a NaN in
- * the query counts as 0.  (Not so
- * where sum_c |q_c bounds_c| is past 2^126 or below 2^-100: which of the pages with such sums are kept is then undefined.)
+ * the query counts as 0.  An infinite bound counts as the formula has it (0 times infinity is not a number).  The bounds are
+ * those of tq_append_pages: [0] nowhere above [1].  (Which pages are kept is undefined among those where the finite terms
+ * of sum_c |q_c bounds_c| add up to more than 2^126 or less than 2^-100, and for an infinite query.)
  * Calls that overlap on the GPU must use distinct workspaces.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim, dtype, GQA group > 8, 2^39 pages or more in all rows).
  */

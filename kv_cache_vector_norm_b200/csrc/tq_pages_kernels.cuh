@@ -639,6 +639,8 @@ __device__ __forceinline__ int64_t select_len(const SelectParams& p, int b) {
 // q_g . k for every key in the page.  With lo <= hi the larger product is (q > 0 ? q hi : q lo), so U_g is the product
 // of max(q, 0) with hi plus that of min(q, 0) with lo.  Products of 16-bit values are exact in fp32, and the order in
 // which they are added up is part of the operator, so that the choice of pages can be reproduced bit for bit.
+// With an infinite bound that sum of two products can be 0 times infinity where U_g is a number; pages that come out as not a
+// number get their scores from the definition.
 //
 // The tensor cores add in an order of their own, but nothing else is fast enough to keep up with the memory: on the
 // FMA pipe with that order 8192 pages x 8 kv heads x 8 query heads take 13 us, here 4.5.  So every score is first
@@ -651,6 +653,36 @@ __device__ __forceinline__ int64_t select_len(const SelectParams& p, int b) {
 // 17 d / 32 2^-23 of the chains' sizes, which add up to the row's.  Three more additions join the chains.
 template <int D>
 constexpr float kScoreError = (17.f * D / 32.f + 7.f) / 8388608.f;
+
+// The key of page `id` by its score in the defined order, by a whole warp: each 8 channels as an even and an odd chain,
+// the two added, then the upper half of the sums onto the lower.  q: the group's heads.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t exact_key(const SelectParams& p, int h, int id, const uint4* q) {
+    constexpr int LP = D / 8;                            // lanes with channels; the others repeat theirs
+    const int l = (threadIdx.x & 31) % LP;
+    const T* page = static_cast<const T*>(p.bounds) + (static_cast<int64_t>(id) * p.heads + h) * 2 * D;
+    const uint4 lw = *reinterpret_cast<const uint4*>(page + 8 * l), hw = *reinterpret_cast<const uint4*>(page + D + 8 * l);
+    const uint32_t lo[4] = {lw.x, lw.y, lw.z, lw.w}, hi[4] = {hw.x, hw.y, hw.z, hw.w};
+    float best = -INFINITY;
+#pragma unroll 4
+    for (int g = 0; g < p.group; ++g) {
+        const uint4 qw = q[g * LP + l];
+        const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Pair<T>::floats(x[i]), a = Pair<T>::floats(lo[i]), c = Pair<T>::floats(hi[i]);
+            const float qe = f.x == f.x ? f.x : 0.f, qo = f.y == f.y ? f.y : 0.f;
+            even += max_nan(qe * a.x, qe * c.x);
+            odd += max_nan(qo * a.y, qo * c.y);
+        }
+        float s = even + odd;
+#pragma unroll
+        for (int o = LP / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        best = max_nan(best, s);
+    }
+    return score_key(best);
+}
 
 // Keys of the cnt pages from p0 on of a row of nb pages by the whole block, and the largest size among them (returned
 // to every thread of the warp that saw it).  ids: the pages' ids.  A warp takes 16 pages as the rows of its MMAs; head g
@@ -738,35 +770,24 @@ __device__ __forceinline__ float score_pages(const SelectParams& p, int b, int h
     return size;
 }
 
-// The key of page `id` by its score in the defined order, by a whole warp: each 8 channels as an even and an odd chain,
-// the two added, then the upper half of the sums onto the lower.  q: the group's heads, in shared memory.
-template <typename T, int D>
-__device__ __forceinline__ uint32_t exact_key(const SelectParams& p, int h, int id, const uint4* q) {
-    constexpr int LP = D / 8;                            // lanes with channels; the others repeat theirs
-    const int l = (threadIdx.x & 31) % LP;
-    const T* page = static_cast<const T*>(p.bounds) + (static_cast<int64_t>(id) * p.heads + h) * 2 * D;
-    const uint4 lw = *reinterpret_cast<const uint4*>(page + 8 * l), hw = *reinterpret_cast<const uint4*>(page + D + 8 * l);
-    const uint32_t lo[4] = {lw.x, lw.y, lw.z, lw.w}, hi[4] = {hw.x, hw.y, hw.z, hw.w};
-    float best = -INFINITY;
-#pragma unroll 4
-    for (int g = 0; g < p.group; ++g) {
-        const uint4 qw = q[g * LP + l];
-        const uint32_t x[4] = {qw.x, qw.y, qw.z, qw.w};
-        float even = 0.f, odd = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = Pair<T>::floats(x[i]), a = Pair<T>::floats(lo[i]), c = Pair<T>::floats(hi[i]);
-            even = fmaf(fmaxf(f.x, 0.f), c.x, even);
-            even = fmaf(fminf(f.x, 0.f), a.x, even);
-            odd = fmaf(fmaxf(f.y, 0.f), c.y, odd);
-            odd = fmaf(fminf(f.y, 0.f), a.y, odd);
-        }
-        float s = even + odd;
-#pragma unroll
-        for (int o = LP / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        best = max_nan(best, s);
+// The keys of a row's nb pages whose scores came out as not a number, from the definition, by NT threads.  table: the row's page ids.
+// Rarely called, and apart, so that it takes no registers elsewhere.
+template <typename T, int D, int NT>
+__device__ __noinline__ void score_by_definition(const void* bounds, const uint4* q, const int32_t* table, int heads, int group, int num_pages,
+                                                 int h, int nb, uint32_t* keys) {
+    SelectParams p;
+    p.bounds = bounds;
+    p.heads = heads;
+    p.group = group;
+#pragma unroll 1
+    for (int j = threadIdx.x >> 5; j < nb; j += NT / 32) {
+        if (keys[j] != 0u) continue;                     // a number, or kept in any case
+        const int id = table[j];
+        const uint32_t key = id < 0 || id >= num_pages ? 0u : exact_key<T, D>(p, h, id, q);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) keys[j] = key;
     }
-    return score_key(best);
+    __syncthreads();
 }
 
 // Keys of a call with few rows, where a CTA per row would leave most of the GPU idle: a CTA per row and p.tile pages.
@@ -899,7 +920,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     };
     const uint32_t wanted = static_cast<uint32_t>(p.budget - p.keep_first - p.keep_last);   // of those that compete
     uint32_t from = 0xffffffffu, bound = 0xffffffffu, need = 0;      // in: keys from `from` on, and `need` equal to `bound`
-    // The range of the block's keys; from each thread the smallest and largest of its own.
+    // The range of the block's keys, and whether one of them is no number; from each thread the smallest and largest of its own.
     auto block_range = [&](uint32_t& least, uint32_t& most) {
         uint32_t low = __reduce_min_sync(0xffffffffu, least), high = __reduce_max_sync(0xffffffffu, most);
         uint32_t best = __reduce_min_sync(0xffffffffu, most);
@@ -913,9 +934,11 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
         least = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0xffffffffu);
         most = __reduce_max_sync(0xffffffffu, lane < NW ? s_warp2[lane] : 0u);
         best = __reduce_min_sync(0xffffffffu, lane < NW ? s_warp3[lane] : 0xffffffffu);
+        const bool none = least == 0u;
         // every thread has a key from the smallest of the threads' largest ones on: if no more are wanted, it ends there
         if (best > 0u && need <= NT) least = best - 1u;
         --most;
+        return none;
     };
     if (wanted > 0) {
         need = wanted;
@@ -923,7 +946,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
         for (int o = 16; o; o >>= 1) error = fmaxf(error, __shfl_xor_sync(0xffffffffu, error, o));
         error *= 2.f * kScoreError<D>;
         int bits = 32;
-        bool exact = false;
+        bool exact = false, defined = false;             // defined: no score that is a number by the definition counts as none
         for (bool again = true; again;) {
             if (bits == 32) {
                 // the range of the keys that compete
@@ -932,7 +955,11 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
                     least = min(least, k);
                     most = max(most, k + 1u);            // kKept: 0
                 });
-                block_range(least, most);
+                if (block_range(least, most) && !defined && !exact) {
+                    defined = true;
+                    score_by_definition<T, D, NT>(p.bounds, s_q, table, p.heads, p.group, p.num_pages, h, nb, keys);
+                    continue;
+                }
                 bound = least;
                 bits = 32 - __clz(static_cast<int>(most - least));
             }

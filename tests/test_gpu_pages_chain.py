@@ -153,3 +153,37 @@ def test_attend_pages_accuracy(dtype, d, b, width):
     got = np64(tq.attend_pages(q, kp, vp, i32(table), i32(lens)))
     want, _ = po.attend(np64(q), np64(kp), np64(vp), table, lens, d ** -0.5)
     assert po.row_error(got, want).max() <= po.ROW_RTOL, po.row_error(got, want).max()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("b,n", [(40, 150), (3, 700)])
+def test_select_with_infinite_bounds(dtype, d, b, n):
+    """Keys that are infinite in a channel: a page's score is what the formula gives (finite, infinite, or not a number where
+    infinities of both signs or 0 * infinity meet), by one kernel and by two."""
+    rng = np.random.default_rng(d + b)
+    gen = torch.Generator(device=DEV).manual_seed(d + b)
+    h, g, num = 2, 3, 900
+    bounds = page_bounds(gen, num, h, d, DTYPES[dtype])
+    kind = torch.as_tensor(rng.integers(0, 12, (num, h)), device=DEV)      # half of the pages have an infinite bound
+    channel = torch.as_tensor(rng.integers(0, d, (num, h, 2)), device=DEV)
+    for e in range(num):
+        for j in range(h):
+            k, (x, y) = int(kind[e, j]), channel[e, j].tolist()
+            if k in (0, 1):
+                bounds[e, j, 0, x] = -torch.inf
+            if k in (2, 1):
+                bounds[e, j, 1, x] = torch.inf
+            if k == 3:
+                bounds[e, j, :, x] = -torch.inf
+            if k == 4:
+                bounds[e, j, 0, x], bounds[e, j, 0, y] = -torch.inf, -torch.inf
+            if k == 5:
+                bounds[e, j, :, x], bounds[e, j, 1, y] = -torch.inf, torch.inf
+    q = torch.randn((b, h * g, d), generator=gen, device=DEV).to(DTYPES[dtype])
+    q[0, 0, :d // 2] = 0
+    table = np.stack([rng.permutation(num)[:n] for _ in range(b)])
+    lens = rng.integers(16 * n // 2, 16 * n + 1, b)
+    with np.errstate(invalid="ignore"):
+        for budget in (12, n // 3):
+            check_select(q, bounds, table, lens, budget, 1, 1)
