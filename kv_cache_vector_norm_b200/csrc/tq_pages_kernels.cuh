@@ -886,6 +886,7 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     const int part = SCORED ? blockIdx.y : 0;
     if (tid == 0 && part == 0) p.lens[row] = static_cast<int>(nb <= p.budget ? len : len - static_cast<int64_t>(nb - p.budget) * kPage);
     if (nb <= p.budget) {                                // every page is kept
+        if constexpr (SCORED) asm volatile("cp.async.wait_all;" ::: "memory");       // no copy outlives its CTA
         if (part == 0)
             for (int j = tid; j < p.budget; j += NT) out[j] = head_page(j < nb ? table[j] : -1);
         return;
