@@ -1102,7 +1102,8 @@ __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED 
     // the part's warps take equal runs of key groups, which begin in the chunk of warp `in_chunk` of the sums above
     const int parts = SCORED ? p.parts : 1, groups = chunk / kKeyGroup, run = (groups + parts - 1) / parts;
     const int part_end = (part + 1) * (NW / parts) * groups, g0 = part * (NW / parts) * groups + warp * run;
-    const int g1 = g0 + run < part_end ? g0 + run : part_end, in_chunk = g0 / groups;
+    const int g1 = g0 + run < part_end ? g0 + run : part_end;
+    const int in_chunk = g0 < part_end ? g0 / groups : 0;            // warps behind the part's last run have none
     uint32_t in_before = __reduce_add_sync(0xffffffffu, lane < in_chunk ? s_warp[lane] : 0u);
     uint32_t ties_before = __reduce_add_sync(0xffffffffu, lane < in_chunk ? s_warp2[lane] : 0u);
     const unsigned lower = (1u << lane) - 1u;            // the lanes before
