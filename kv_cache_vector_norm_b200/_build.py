@@ -1,11 +1,13 @@
 """Build libtq.so (the C-ABI library) in-tree with nvcc for sm_100a, and _bind.so (the compiled part of its Python
 binding) against the installed torch.
 
-Usage: ``python -m kv_cache_vector_norm_b200._build [--force] [--verbose]``.  The library is rebuilt
-when any source under csrc/ or include/ is newer than the existing .so.
+Usage: ``python -m kv_cache_vector_norm_b200._build [--force] [--verbose]``.  The library is rebuilt when any of its
+sources under csrc/ or include/ is newer than the existing .so, the binding when its source is newer or it was compiled against
+another torch or Python (its stamp, beside it, says which).
 """
 from __future__ import annotations
 
+import json
 import os
 import subprocess
 import sys
@@ -18,6 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_SOURCE = "tq_bind.cpp"
+BIND_STAMP = os.path.join(PKG, "_bind.stamp")           # what the binding was compiled against
+BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -31,11 +36,42 @@ def _sources():
     return out
 
 
+def _read(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
+def _write(path: str, text: str) -> None:
+    with open(path, "w") as f:
+        f.write(text)
+
+
+def _newer(path: str, sources) -> bool:
+    """Whether a file is there and no source is newer."""
+    return os.path.exists(path) and all(os.path.getmtime(s) <= os.path.getmtime(path) for s in sources)
+
+
+def _bind_needs() -> str:
+    """What a binding is tied to: the torch it is compiled against, its C++ ABI, and Python's."""
+    import torch
+
+    return json.dumps(dict(torch=torch.__version__, cxx11_abi=bool(torch._C._GLIBCXX_USE_CXX11_ABI),
+                           python=sysconfig.get_config_var("SOABI")))
+
+
+def _lib_current() -> bool:
+    return _newer(LIB, [s for s in _sources() if os.path.basename(s) != BIND_SOURCE])
+
+
+def _bind_current() -> bool:
+    return (_newer(BIND, [os.path.join(CSRC, BIND_SOURCE), os.path.join(INCLUDE, "tq.h")]) and
+            _read(BIND_STAMP) == _bind_needs())
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return any(os.path.getmtime(s) > t for s in _sources())
+    return not (_lib_current() and _bind_current())
 
 
 # source -> (its kind, the files under csrc/ it is compiled from besides tq.h and tq_internal.h)
@@ -66,7 +102,7 @@ def _build_bind(verbose: bool) -> None:
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-           f"-I{sysconfig.get_paths()['include']}", "-I/usr/local/cuda/include", os.path.join(CSRC, "tq_bind.cpp"), "-o",
+           f"-I{sysconfig.get_paths()['include']}", "-I/usr/local/cuda/include", os.path.join(CSRC, BIND_SOURCE), "-o",
            BIND + ".tmp", f"-L{PKG}", "-l:libtq.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python"]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -75,31 +111,27 @@ def _build_bind(verbose: bool) -> None:
     if r.returncode:
         raise RuntimeError("compiling tq_bind.cpp failed")
     os.replace(BIND + ".tmp", BIND)
+    _write(BIND_STAMP, _bind_needs())
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not needs_build():
-        return LIB
-    build_dir = os.path.join(PKG, "_build")
-    os.makedirs(build_dir, exist_ok=True)
+def _build_lib(force: bool, verbose: bool, extra) -> None:
+    os.makedirs(BUILD_DIR, exist_ok=True)
     common = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", f"-I{INCLUDE}"]
     objs = []
     cmds = []
     for src, (kind, _) in UNITS.items():
-        obj = os.path.join(build_dir, src + ".o")
+        obj = os.path.join(BUILD_DIR, src + ".o")
         objs.append(obj)
-        if not force and not extra and _fresh(obj, src):
-            continue
         if kind == "cu":
             cmd = [nvcc(), *ARCH_FLAGS, *common, "-Xptxas", "-warn-spills", *extra, "-c",
                    os.path.join(CSRC, src), "-o", obj]
         else:
             cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", f"-I{INCLUDE}",
                    "-I/usr/local/cuda/include", "-c", os.path.join(CSRC, src), "-o", obj]
-        cmds.append(cmd)
-    t0 = time.time()
-    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
-    for c, p in zip(cmds, procs):
+        if force or extra or not _fresh(obj, src):
+            cmds.append((obj, cmd))
+    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for _, c in cmds]
+    for (obj, c), p in zip(cmds, procs):
         out, _ = p.communicate()
         if verbose or p.returncode:
             sys.stderr.write(" ".join(c) + "\n" + out)
@@ -112,9 +144,17 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         sys.stderr.write(" ".join(link) + "\n" + r.stdout)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
-    _build_bind(verbose)
-    if verbose:
-        sys.stderr.write(f"built {LIB} in {time.time() - t0:.1f}s\n")
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    t0 = time.time()
+    lib, bind = force or not _lib_current(), force or not _bind_current()
+    if lib:
+        _build_lib(force, verbose, extra)
+    if bind:
+        _build_bind(verbose)
+    if verbose and (lib or bind):
+        sys.stderr.write(f"built {LIB if lib else BIND} in {time.time() - t0:.1f}s\n")
     return LIB
 
 
