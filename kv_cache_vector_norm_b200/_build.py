@@ -2,8 +2,8 @@
 binding) against the installed torch.
 
 Usage: ``python -m kv_cache_vector_norm_b200._build [--force] [--verbose]``.  The library is rebuilt when any of its
-sources under csrc/ or include/ is newer than the existing .so, the binding when its source is newer or it was compiled against
-another torch or Python (its stamp, beside it, says which).
+sources under csrc/ or include/ is newer than the existing .so or it was compiled with other flags, the binding when its
+source is newer or it was compiled against another torch or Python (its stamp, beside it, says which).
 """
 from __future__ import annotations
 
@@ -23,6 +23,7 @@ BIND = os.path.join(PKG, "_bind.so")
 BIND_SOURCE = "tq_bind.cpp"
 BIND_STAMP = os.path.join(PKG, "_bind.stamp")           # what the binding was compiled against
 BUILD_DIR = os.path.join(PKG, "_build")
+LIB_FLAGS = os.path.join(BUILD_DIR, "libtq.flags")       # extra flags of the library (unknown if the file is not there)
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -61,8 +62,10 @@ def _bind_needs() -> str:
                            python=sysconfig.get_config_var("SOABI")))
 
 
-def _lib_current() -> bool:
-    return _newer(LIB, [s for s in _sources() if os.path.basename(s) != BIND_SOURCE])
+def _lib_current(extra=()) -> bool:
+    flags = _read(LIB_FLAGS)
+    return (_newer(LIB, [s for s in _sources() if os.path.basename(s) != BIND_SOURCE]) and
+            (flags == json.dumps(list(extra)) or (flags is None and not extra)))
 
 
 def _bind_current() -> bool:
@@ -82,9 +85,9 @@ UNITS = {
 }
 
 
-def _fresh(obj: str, src: str) -> bool:
-    """Whether an object file is newer than everything it is compiled from."""
-    if not os.path.exists(obj):
+def _fresh(obj: str, src: str, cmd) -> bool:
+    """Whether an object file was compiled by this command and is newer than everything it is compiled from."""
+    if not os.path.exists(obj) or _read(obj + ".cmd") != json.dumps(cmd):
         return False
     deps = [os.path.join(CSRC, n) for n in (src, "tq_internal.h", *UNITS[src][1])] + [os.path.join(INCLUDE, "tq.h")]
     return all(os.path.getmtime(d) < os.path.getmtime(obj) for d in deps)
@@ -128,7 +131,7 @@ def _build_lib(force: bool, verbose: bool, extra) -> None:
         else:
             cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", f"-I{INCLUDE}",
                    "-I/usr/local/cuda/include", "-c", os.path.join(CSRC, src), "-o", obj]
-        if force or extra or not _fresh(obj, src):
+        if force or not _fresh(obj, src, cmd):
             cmds.append((obj, cmd))
     procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for _, c in cmds]
     for (obj, c), p in zip(cmds, procs):
@@ -137,6 +140,7 @@ def _build_lib(force: bool, verbose: bool, extra) -> None:
             sys.stderr.write(" ".join(c) + "\n" + out)
         if p.returncode:
             raise RuntimeError(f"compilation failed: {' '.join(c[:2])} ...")
+        _write(obj + ".cmd", json.dumps(c))
     tmp = LIB + ".tmp"
     link = [nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-lpthread", "-ldl"]
     r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -144,11 +148,12 @@ def _build_lib(force: bool, verbose: bool, extra) -> None:
         sys.stderr.write(" ".join(link) + "\n" + r.stdout)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    _write(LIB_FLAGS, json.dumps(list(extra)))
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     t0 = time.time()
-    lib, bind = force or not _lib_current(), force or not _bind_current()
+    lib, bind = force or not _lib_current(extra), force or not _bind_current()
     if lib:
         _build_lib(force, verbose, extra)
     if bind:

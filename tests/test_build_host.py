@@ -1,4 +1,4 @@
-"""When the library and its Python binding are rebuilt: after a change of torch or of Python, of sources.  Compilers are
+"""When the library and its Python binding are rebuilt: after a change of torch or of Python, of flags, of sources.  Compilers are
 stood in for by a function that writes the output file."""
 import os
 import types
@@ -19,7 +19,8 @@ def tree(tmp_path, monkeypatch):
         f.write_text("")
         os.utime(f, (1000, 1000))
     for name, at in dict(PKG=tmp_path, CSRC=csrc, INCLUDE=include, LIB=tmp_path / "libtq.so", BIND=tmp_path / "_bind.so",
-                         BIND_STAMP=tmp_path / "_bind.stamp", BUILD_DIR=tmp_path / "_build").items():
+                         BIND_STAMP=tmp_path / "_bind.stamp", BUILD_DIR=tmp_path / "_build",
+                         LIB_FLAGS=tmp_path / "_build" / "libtq.flags").items():
         monkeypatch.setattr(_build, name, str(at))
     ran = []
 
@@ -58,6 +59,18 @@ def test_another_torch_or_python_rebuilds_the_binding_alone(tree, monkeypatch, w
     assert _build.needs_build()
     _build.build()
     assert tree.sources() == [_build.BIND_SOURCE] and not _build.needs_build()
+
+
+def test_objects_of_other_flags_are_not_linked_in(tree):
+    _build.build()
+    tree.ran.clear()
+    _build.build(extra=("-DSOMETHING",))
+    cu = [n for n, (kind, _) in _build.UNITS.items() if kind == "cu"]
+    assert sorted(tree.sources()) == sorted(cu) and all("-DSOMETHING" in c for c in tree.ran if "-c" in c)
+    assert _build.needs_build()
+    tree.ran.clear()
+    _build.build()
+    assert sorted(tree.sources()) == sorted(cu) and not any("-DSOMETHING" in c for c in tree.ran) and not _build.needs_build()
 
 
 def test_a_source_rebuilds_what_is_made_of_it(tree):
