@@ -77,6 +77,9 @@ int64_t integer(PyObject* o) {
     return v;
 }
 
+// The stride of a dimension, or `dense` where it has one entry or none: its stride there says nothing, and may be anything.
+int64_t stride(const at::Tensor& t, int64_t dim, int64_t dense) { return t.size(dim) > 1 ? t.stride(dim) : dense; }
+
 // Sizes go through int fields: what does not fit is given as -1, which every entry point refuses.
 int as_int(int64_t v) { return v >= 0 && v <= INT32_MAX ? static_cast<int>(v) : -1; }
 
@@ -158,15 +161,15 @@ PyObject* append_pages(PyObject* const* v, Py_ssize_t n) {
     a.num_pages = as_int(pages);
     a.num_tokens = rows;
     a.k = k.data_ptr();
-    a.k_token_stride = k.stride(0);
-    a.k_head_stride = k.stride(1);
+    a.k_token_stride = stride(k, 0, heads * d);
+    a.k_head_stride = stride(k, 1, d);
     if (v[1] != Py_None) {
         const at::Tensor& t = tensor(v[1], "v");
         same(t, "v", k.scalar_type(), dev);
         if (t.sizes() != k.sizes() || t.stride(2) != 1) refuse(PyExc_ValueError, "v must be [N, H_kv, d] like k, with unit stride along d");
         a.v = t.data_ptr();
-        a.v_token_stride = t.stride(0);
-        a.v_head_stride = t.stride(1);
+        a.v_token_stride = stride(t, 0, heads * d);
+        a.v_head_stride = stride(t, 1, d);
     } else if (v[4] != Py_None) {
         refuse(PyExc_ValueError, "v_pool needs v");
     }
@@ -181,7 +184,7 @@ PyObject* append_pages(PyObject* const* v, Py_ssize_t n) {
 const at::Tensor& query(PyObject* o) {
     const at::Tensor& q = cuda_tensor(o, "q");
     page_dtype(q, "q");
-    if (q.dim() != 3 || q.stride(2) != 1 || (q.size(1) > 1 && q.stride(1) != q.size(2)))
+    if (q.dim() != 3 || q.stride(2) != 1 || stride(q, 1, q.size(2)) != q.size(2))
         refuse(PyExc_ValueError, "q must be [B, H_q, d] with contiguous heads");
     return q;
 }
@@ -207,7 +210,7 @@ PyObject* select_pages(PyObject* const* v, Py_ssize_t n) {
     a.keep_first = as_int(integer(v[8]));
     a.keep_last = as_int(integer(v[9]));
     a.q = q.data_ptr();
-    a.q_stride = q.stride(0);
+    a.q_stride = stride(q, 0, q.size(1) * d);
     a.bounds = need<void>(v[1], "bounds", q.scalar_type(), {pages, heads, 2, d}, dev);
     a.block_table = need<int32_t>(v[2], "block_table", at::kInt, {b, width}, dev);
     a.seq_lens = need<int32_t>(v[3], "seq_lens", at::kInt, {b}, dev);
@@ -238,7 +241,7 @@ PyObject* attend_pages(PyObject* const* v, Py_ssize_t n) {
     const std::initializer_list<int64_t> shape = {pages, heads, kPage, d};
     auto pool = [&](const at::Tensor& t, const char* name) {         // each page contiguous, pages may lie apart
         same(t, name, q.scalar_type(), dev);
-        if (t.sizes() != at::IntArrayRef(shape) || t.stride(3) != 1 || t.stride(2) != d || t.stride(1) != kPage * d)
+        if (t.sizes() != at::IntArrayRef(shape) || t.stride(3) != 1 || t.stride(2) != d || stride(t, 1, kPage * d) != kPage * d)
             refuse(PyExc_ValueError, std::string(name) + " must be " + list(at::IntArrayRef(shape)) + ", each page contiguous; got " +
                                          list(t.sizes()) + ", strides " + list(t.strides()));
         return t.data_ptr();
@@ -255,11 +258,11 @@ PyObject* attend_pages(PyObject* const* v, Py_ssize_t n) {
     a.scale = static_cast<float>(PyFloat_AsDouble(v[7]));
     if (PyErr_Occurred()) throw Refused();
     a.q = q.data_ptr();
-    a.q_stride = q.stride(0);
+    a.q_stride = stride(q, 0, q.size(1) * d);
     a.k_pool = pool(kp, "k_pool");
     a.v_pool = pool(vp, "v_pool");
-    a.k_page_stride = kp.stride(0);
-    a.v_page_stride = vp.stride(0);
+    a.k_page_stride = stride(kp, 0, heads * kPage * d);
+    a.v_page_stride = stride(vp, 0, heads * kPage * d);
     if (a.selected) {
         a.block_table = need<int32_t>(v[3], "block_table", at::kInt, {b, heads, width}, dev);
         a.seq_lens = need<int32_t>(v[4], "seq_lens", at::kInt, {b, heads}, dev);

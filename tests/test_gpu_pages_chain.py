@@ -187,3 +187,41 @@ def test_select_with_infinite_bounds(dtype, d, b, n):
     with np.errstate(invalid="ignore"):
         for budget in (12, n // 3):
             check_select(q, bounds, table, lens, budget, 1, 1)
+
+
+def last_first(t):
+    """A tensor with a leading dimension of one entry whose stride is 1: contiguous, as torch counts."""
+    return t.contiguous()[..., None].movedim(-1, 0)
+
+
+def test_strides_of_dimensions_of_one_entry():
+    """A dimension of one entry has no step: whatever stride it carries is not looked at."""
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    g, d, n = 4, 64, 40
+    kp, vp = pools(gen, 3, 1, d, torch.float16)
+    bounds = torch.stack((kp.amin(2), kp.amax(2)), 2).contiguous()
+    q = torch.randn((1, g, d), generator=gen, device=DEV).half()
+    table, lens = i32([[2, 0, 1]]), i32([n])
+    want = tq.attend_pages(q, kp, vp, table, lens)
+    odd_q = last_first(q[0])
+    odd_k, odd_v = (t[:, 0].contiguous()[..., None].movedim(-1, 1) for t in (kp, vp))                  # one head
+    assert odd_q.stride(0) == 1 and odd_k.stride(1) == 1 and odd_q.is_contiguous() and odd_k.is_contiguous()
+    assert torch.equal(tq.attend_pages(odd_q, odd_k, odd_v, table, lens), want)
+    for a, b in zip(tq.select_pages(odd_q, bounds, table, lens, budget=2), tq.select_pages(q, bounds, table, lens, budget=2)):
+        assert torch.equal(a, b)
+    one = [last_first(t[2]) for t in (kp, vp)]                                                         # one page
+    lists, tokens = i32([[[0]]]), i32([[16]])
+    assert one[0].stride(0) == 1 and torch.equal(tq.attend_pages(q, *one, lists, tokens), tq.attend_pages(q, kp, vp, i32([[[2]]]), tokens))
+    far = torch.stack((kp, vp), 1)[2:]                                                                 # one page of a joint pool
+    assert torch.equal(tq.attend_pages(q, far[:, 0], far[:, 1], lists, tokens), tq.attend_pages(q, kp, vp, i32([[[2]]]), tokens))
+    for h, rows in ((3, 1), (1, 5), (1, 1)):
+        k, v = torch.randn((2, rows, h, d), generator=gen, device=DEV).half()
+        odd = [last_first(t[0]) if rows == 1 else t[:, 0].contiguous()[..., None].movedim(-1, 1) for t in (k, v)]
+        assert 1 in odd[0].stride()[:2]
+        slots = torch.arange(rows * h, device=DEV) * 16
+        got, ref = ([torch.zeros((rows, h, 16, d), device=DEV).half() for _ in range(2)] for _ in range(2))
+        near = [torch.zeros((rows, h, 2, d), device=DEV).half() for _ in range(2)]
+        tq.append_pages(*odd, slots, k_pool=got[0], v_pool=got[1], bounds=near[0])
+        tq.append_pages(k, v, slots, k_pool=ref[0], v_pool=ref[1], bounds=near[1])
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]) and torch.equal(*near)
+        assert torch.equal(got[0].view(-1, d)[slots], k.view(-1, d))
