@@ -401,14 +401,27 @@ def _window(win_k: torch.Tensor, win_v: torch.Tensor, win_lens: torch.Tensor | N
 def _attend_args(codec: Codec, q, cache: Cache, *, num_kv_heads, v_bits, v_group, max_seq_len, block_table,
                  seq_lens, scale, out, workspace):
     b, hq, d = q.shape
+    if out is not None or workspace is not None:         # a call, not a question of size: elements are read as they lie
+        for t, name, dtype in ((q, "q", torch.float16), (block_table, "block_table", torch.int32),
+                               (seq_lens, "seq_lens", torch.int32), (out, "out", torch.float32)):
+            if t is not None:
+                _need_cuda(t, name, dtype)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
     if block_table is not None and block_table.dim() == 3:
         # pages selected for each kv head (select_pages): every (sequence, kv head) is a sequence of one kv head
         if block_table.shape[:2] != (b, num_kv_heads) or seq_lens is None or seq_lens.shape != (b, num_kv_heads):
             raise ValueError("selected pages need block_table [B, H_kv, n] and seq_lens [B, H_kv]")
-        if hq % num_kv_heads or not (q.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous()):
-            raise ValueError("selected pages need contiguous q, block_table and seq_lens, and H_q a multiple of H_kv")
+        if hq % num_kv_heads:
+            raise ValueError("selected pages need H_q to be a multiple of H_kv")
         b, hq, num_kv_heads = b * num_kv_heads, hq // num_kv_heads, 1
         block_table = block_table.view(b, -1)
+    elif block_table is not None and (block_table.dim() != 2 or block_table.shape[0] != b):
+        raise ValueError("block_table must be [B, n], or [B, H_kv, n] for selected pages")
+    elif seq_lens is not None and seq_lens.shape != (b,):
+        raise ValueError("seq_lens must be [B]")
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
     a = AttendArgs()
     a.batch, a.num_q_heads, a.num_kv_heads, a.head_dim = b, hq, num_kv_heads, d
     a.v_bits, a.v_group, a.scale = v_bits, v_group, float(scale)

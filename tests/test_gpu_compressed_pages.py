@@ -192,3 +192,45 @@ def test_a_selection_with_pages_that_are_none():
     got = np64(c.attend(q, h, block_table=pages, seq_lens=tokens))
     ref, _ = po.attend(np64(q), k, v, pages.cpu().numpy(), tokens.cpu().numpy(), d ** -0.5, True)
     assert np.linalg.norm(got - ref) <= L2_RTOL * np.linalg.norm(ref)
+
+
+def test_operands_that_would_be_misread_are_refused():
+    """Types, layouts and shapes of the query, the table, the lengths and the output that the kernels would read as something else
+    are refused on the host, by every reader."""
+    b, h, g, d, n, num = 2, 2, 4, 64, 3, 8
+    c = Compressed(num * h * 16, d, 4, 4, 32)
+    r = Compressed(num * h * 16, d, 3, 4, 32, qjl=True)
+    q = torch.zeros((b, h * g, d), dtype=torch.float16, device=DEV)
+    wide = torch.zeros((b, h * g + 2 * h, d), dtype=torch.float16, device=DEV)
+    table, lens = i32(np.zeros((b, n))), i32([16, 20])
+    lists, tokens = i32(np.zeros((b, h, n))), i32(np.full((b, h), 16))
+    out = torch.zeros((b, h * g, d), device=DEV)
+
+    def decode(q, out=out, **kw):
+        return tq.attend_decode(c.codec, q, c.cache, num_kv_heads=h, out=out, **c.kw, **kw)
+
+    def noalloc(q, out=out, **kw):
+        return tq.attend_decode_noalloc(c.codec, q, c.cache, num_kv_heads=h, out=out, **c.kw, **kw)
+
+    def qjl(q, out=out, **kw):
+        return r.attend(q, h, out=out, **kw)
+
+    def scores(q, out=None, **kw):
+        return tq.attend_scores(c.codec, q, c.cache, num_kv_heads=h, **c.kw, **kw)
+
+    bad = [(TypeError, "block_table", dict(block_table=table.long())), (TypeError, "seq_lens", dict(seq_lens=lens.long())),
+           (ValueError, "q must be contiguous", dict(q=wide[:, :h * g])), (TypeError, "block_table", dict(block_table=table.cpu())),
+           (ValueError, "block_table must be contiguous", dict(block_table=i32(np.zeros((n, b))).t())),
+           (ValueError, "seq_lens must be contiguous", dict(seq_lens=i32([1, 1, 1, 1])[::2])),
+           (ValueError, "block_table must be", dict(block_table=i32(np.zeros((1, n))))),
+           (ValueError, "seq_lens must be", dict(seq_lens=i32([16, 16, 16]))), (ValueError, "seq_lens must be", dict(seq_lens=tokens)),
+           (ValueError, "selected pages need", dict(block_table=lists)),
+           (ValueError, "selected pages need", dict(block_table=lists[:, :1].contiguous(), seq_lens=tokens))]
+    bad_out = [(TypeError, "out", dict(out=out.half())), (ValueError, "out must be contiguous", dict(out=torch.zeros((b, h * g, 2 * d), device=DEV)[:, :, :d])),
+               (ValueError, "shape of q", dict(out=out[:1]))]
+    for read in (decode, noalloc, qjl, scores):
+        read(q, block_table=table, seq_lens=lens), read(q, block_table=lists, seq_lens=tokens)
+        for kind, what, kw in bad + (bad_out if read is not scores else []):
+            with pytest.raises(kind, match=what):
+                read(**{**dict(q=q, block_table=table, seq_lens=lens), **kw})
+    torch.cuda.synchronize()
