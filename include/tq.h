@@ -215,9 +215,9 @@ tq_status tq_decode_v(int d, int bits, int group, const uint8_t* data, const voi
  * pool behind a sequence's last token may hold anything.  Query head hq reads kv head hq / (num_q_heads / num_kv_heads).
  */
 typedef struct tq_attend_args {
-    int batch;                 /* B >= 1 */
+    int batch;                 /* B, 1 .. 65535 */
     int num_q_heads;           /* H_q, a multiple of num_kv_heads; H_q / H_kv <= 8 */
-    int num_kv_heads;          /* H_kv >= 1 */
+    int num_kv_heads;          /* H_kv, 1 .. 65535 */
     int head_dim;              /* must equal the codec's d */
     int v_bits;                /* 2, 3, 4 or 8 */
     int v_group;               /* 32 or head_dim */
@@ -537,7 +537,7 @@ tq_status tq_select_pages_workspace_bytes(const tq_select_args* args, size_t* by
  * lens counts the tokens of the listed pages (every page is full but a sequence's last, which is always listed last),
  * so pages and lens are a block table and lengths with one row per (sequence, kv head).  Read them with
  * tq_attend_pages (selected = 1), or with tq_attend_decode on the compressed pools as batch * num_kv_heads sequences
- * of one kv head: a head page is a page of a pool with one kv head.  A listed page whose table entry names no page is
+ * of one kv head (at most 65535 of them): a head page is a page of a pool with one kv head.  A listed page whose table entry names no page is
  * given as -1, which either attention leaves out.
  * Sums run in fp32 in a fixed order (per 8 channels an even and an odd chain, then halves added to halves), so the
  * result is the same on every run and for every shape of the call.  A score that is not a number ranks last; a NaN in

@@ -623,6 +623,9 @@ tq_status plan_attend(const tq_attend_args* a, AttendPlan* plan, bool window = f
     if (!a) return fail(TQ_ERR_INVALID_ARG, "tq_attend: args is NULL");
     if (a->batch < 1 || a->num_kv_heads < 1 || a->num_q_heads < 1)
         return fail(TQ_ERR_INVALID_ARG, "tq_attend: batch, num_q_heads, num_kv_heads must be >= 1");
+    // they are the y and z of a grid
+    if (a->batch > 65535 || a->num_kv_heads > 65535)
+        return fail(TQ_ERR_UNSUPPORTED, "tq_attend: batch=%d, num_kv_heads=%d (at most 65535 of each)", a->batch, a->num_kv_heads);
     if (a->num_q_heads % a->num_kv_heads)
         return fail(TQ_ERR_INVALID_ARG, "tq_attend: num_q_heads=%d is not a multiple of num_kv_heads=%d", a->num_q_heads,
                     a->num_kv_heads);

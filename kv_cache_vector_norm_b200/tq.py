@@ -468,8 +468,8 @@ def attend_decode(codec: Codec, q: torch.Tensor, cache: Cache, *, num_kv_heads: 
                   win_v: torch.Tensor | None = None, win_lens: torch.Tensor | None = None) -> torch.Tensor:
     """One decode step: q [B, H_q, d] fp16 against the compressed cache, plus (win_k, win_v: [B, H_kv, W, d]
     fp16, win_lens: [B] int32 or None) a window of recent uncompressed tokens.  Returns out [B, H_q, d] f32.
-    block_table [B, H_kv, n] with seq_lens [B, H_kv] (select_pages) attends to the selected pages of a paged cache.  Negative
-    entries of a block table are left out; all others up to a row's length must name pages of the cache."""
+    block_table [B, H_kv, n] with seq_lens [B, H_kv] (select_pages) attends to the selected pages of a paged cache (B * H_kv up
+    to 65535).  Negative entries of a block table are left out; all others up to a row's length must name pages of the cache."""
     _need_cuda(q, "q", torch.float16)
     kw = dict(num_kv_heads=num_kv_heads, v_bits=v_bits, v_group=v_group, max_seq_len=max_seq_len,
               block_table=block_table, seq_lens=seq_lens, scale=scale)

@@ -209,3 +209,14 @@ def test_row_tolerance_tells_the_weights_apart(d, n, kind, terms, passes):
         want.append(p @ v / p.sum())
     err = po.row_error(np.stack(got), np.stack(want)).max()
     assert err <= po.ROW_RTOL / 10 if passes else err > 2 * po.ROW_RTOL
+
+
+def test_compressed_attention_takes_as_many_sequences_as_a_grid():
+    """B * H_kv lists of a selection are sequences of one kv head to compressed attention, whose grid holds 65535."""
+    a, nb = tq.AttendArgs(), ctypes.c_size_t()
+    a.batch, a.num_q_heads, a.num_kv_heads, a.head_dim, a.v_bits, a.v_group = 65535, 4, 1, 128, 4, 32
+    a.max_seq_len = 64
+    assert tq.LIB.tq_attend_workspace_bytes(ctypes.byref(a), ctypes.byref(nb)) == tq.TQ_OK
+    a.batch = 65536
+    assert tq.LIB.tq_attend_workspace_bytes(ctypes.byref(a), ctypes.byref(nb)) == tq.TQ_ERR_UNSUPPORTED
+    assert b"65535" in tq.LIB.tq_last_error()
