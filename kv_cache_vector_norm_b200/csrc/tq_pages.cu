@@ -150,11 +150,11 @@ extern "C" tq_status tq_plan_pages(const tq_plan_args* a, void* stream) {
     p.tile = kSlotTile;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Up to 256 requests the slots' grid plans for itself, and its first CTA does the rest if no output lies over an input
-    // (8 heads, 64 requests of one token: 2.4 us, of 64 tokens 2.8).
+    // (8 heads, 64 requests of one token: 2.5 us, of 64 tokens 2.8).
     // Else the rest takes a second kernel, so a decode step's few slots are written by one planning CTA: with 8 heads 64
-    // requests of one token take 3.0 us in one kernel and 3.1 in two (and 2 us less on the host), 256 take 4.4 and 3.3.  Past
-    // 256 requests the slots come behind the plan: 512 take 6.4 us in one kernel and 7.8 in two, 1024 take 10.3 and 7.2.
-    // Up to 256 requests one CTA of 256 threads scans faster than one of 1024 (64 requests: 3.0 us, 5.4).
+    // requests of one token take 3.5 us in one kernel (and 2 us less on the host) and 3.0 in two, 256 take 5.3 and 3.5.  Past
+    // 256 requests the slots come behind the plan: 512 take 7.5 us in one kernel and 8.4 in two, 1024 take 11.8 and 8.6.
+    // Up to 256 requests one CTA of 256 threads scans faster than one of 1024 (64 requests: 3.5 us, 5.7).
     const bool few = a->batch <= kSlotTile;
     p.apart = few && apart(a->seq_lens, a->seq_lens_out, a->batch) && apart(a->free_state, a->free_state_out, 2);
     const int64_t tiles = (a->max_tokens + kSlotTile - 1) / kSlotTile, each = (tiles + device_sms() - 1) / device_sms();
@@ -265,8 +265,9 @@ tq_status plan_select(const char* fn, const tq_select_args* a, SelectPlan* plan)
     const int width = a->max_blocks;
     // With fewer rows than SMs the scores take a grid over all pages; with many rows, or with few pages, a second
     // kernel costs more than it brings, unless a row's keys and page ids do not fit one CTA's shared memory.  Measured
-    // with two kernels and with one, d = 128: 8 rows of 300 pages 8.5 and 9.3 us, of 600 8.2 and 12.6, 128 rows of 300
-    // pages 12.8 and 10.4, of 600 18.2 and 22.8, 512 rows of 600 pages 51.8 and 49.5, of 200 33.0 and 26.2.
+    // with two kernels and with one, d = 128: 8 rows of 300 pages 7.7 and 7.8 us, of 600 8.2 and 10.4, 128 rows of 300
+    // pages 12.3 and 8.6, of 600 17.4 and 16.0, 512 rows of 600 pages 53.7 and 38.1, of 200 33.5 and 20.8.  (So with about as
+    // many rows as SMs one kernel would be as good up to some 700 pages; the rule is from before its loads had the registers.)
     const bool fits = key_stride(width) * 8 <= kSelSmem;
     plan->scored = !fits || (rows < device_sms() && width > 384);
     plan->room = plan->scored && key_stride(width) > kSortRoom ? kSortRoom : static_cast<int>(key_stride(width));

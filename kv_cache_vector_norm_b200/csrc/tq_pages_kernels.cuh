@@ -832,9 +832,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_kernel(const SelectPar
 //
 // The work of one row is bound by the instructions of one SM, a few per key, so keys are read four at a time, what does
 // not compete has a key of its own (no tests of the page's index), and nothing is done per page that is left out.  With
-// few rows several CTAs make a row's choice, each for itself, and write out a part of it (8 rows of 8192 pages: 16.7 us
-// with one, 15.8 with 4, 15.7 with 8, 16.0 with 16).  Without SCORED two CTAs of an SM have the registers that the loads
-// want at d = 128 and 256 (512 rows of 200 pages at d = 128: 20.1 us; three CTAs 26.0), four at d = 64 (10.6; three 13.2).
+// few rows several CTAs make a row's choice, each for itself, and write out a part of it (8 rows of 8192 pages: 16.9 us
+// with one, 15.9 with 4, 15.8 with 8, 16.1 with 16).  Without SCORED two CTAs of an SM have the registers that the loads
+// want at d = 128 and 256 (512 rows of 200 pages: 20.8 and 31.1 us; three CTAs 24.6 and 39.4), four at d = 64 (10.9; three 13.9).
 template <typename T, int D, bool SCORED>
 __global__ void __launch_bounds__(SCORED ? kSortThreads : kScoreThreads, SCORED ? 1 : (D == 64 ? 4 : 2))
     select_kernel(const SelectParams p) {
