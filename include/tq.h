@@ -212,7 +212,8 @@ tq_status tq_decode_v(int d, int bits, int group, const uint8_t* data, const voi
  * past the cache attends to the whole addressable sequence and never reads beyond its rows or its
  * block-table row.  A negative block_table entry names no block: its tokens are left out (of the
  * softmax; their scores are -inf).  Every other entry below the (clamped) length must name a block of the pools.  Rows of a
- * pool behind a sequence's last token may hold anything.  Query head hq reads kv head hq / (num_q_heads / num_kv_heads).
+ * pool behind a sequence's last token may hold anything; a pool holds one block at least.  Query head hq reads kv head
+ * hq / (num_q_heads / num_kv_heads).
  */
 typedef struct tq_attend_args {
     int batch;                 /* B, 1 .. 65535 */

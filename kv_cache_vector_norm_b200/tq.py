@@ -412,8 +412,8 @@ def _attend_args(codec: Codec, q, cache: Cache, *, num_kv_heads, v_bits, v_group
         # pages selected for each kv head (select_pages): every (sequence, kv head) is a sequence of one kv head
         if block_table.shape[:2] != (b, num_kv_heads) or seq_lens is None or seq_lens.shape != (b, num_kv_heads):
             raise ValueError("selected pages need block_table [B, H_kv, n] and seq_lens [B, H_kv]")
-        if hq % num_kv_heads:
-            raise ValueError("selected pages need H_q to be a multiple of H_kv")
+        if hq % num_kv_heads or not block_table.is_contiguous():
+            raise ValueError("selected pages need a contiguous block_table, and H_q to be a multiple of H_kv")
         b, hq, num_kv_heads = b * num_kv_heads, hq // num_kv_heads, 1
         block_table = block_table.view(b, -1)
     elif block_table is not None and (block_table.dim() != 2 or block_table.shape[0] != b):

@@ -225,6 +225,8 @@ def test_operands_that_would_be_misread_are_refused():
            (ValueError, "block_table must be", dict(block_table=i32(np.zeros((1, n))))),
            (ValueError, "seq_lens must be", dict(seq_lens=i32([16, 16, 16]))), (ValueError, "seq_lens must be", dict(seq_lens=tokens)),
            (ValueError, "selected pages need", dict(block_table=lists)),
+           (ValueError, "block_table", dict(block_table=i32(np.zeros((b, n, h))).transpose(1, 2), seq_lens=tokens)),
+           (ValueError, "seq_lens must be contiguous", dict(block_table=lists, seq_lens=i32(np.full((h, b), 16)).t())),
            (ValueError, "selected pages need", dict(block_table=lists[:, :1].contiguous(), seq_lens=tokens))]
     bad_out = [(TypeError, "out", dict(out=out.half())), (ValueError, "out must be contiguous", dict(out=torch.zeros((b, h * g, 2 * d), device=DEV)[:, :, :d])),
                (ValueError, "shape of q", dict(out=out[:1]))]
